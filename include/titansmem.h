@@ -61,7 +61,10 @@ typedef enum {
   TM_ERR_DEVICE = 6        /* the device reported an internal consistency error */
 } tm_status;
 
-typedef enum { TM_ACT_SILU = 0 } tm_act;
+typedef enum {
+  TM_ACT_SILU = 0,
+  TM_ACT_NONE = 1 /* tm_conv and tm_group_norm only; tm_create takes TM_ACT_SILU */
+} tm_act;
 
 typedef enum {
   TM_F32 = 0,  /* k, v, q are float32; fp32 arithmetic throughout            */
@@ -333,6 +336,168 @@ TM_API tm_status tm_prologue(int B, int H, int T, int d, int width, tm_dtype in_
                              const float *filt_k, const float *filt_v, const float *filt_q,
                              const void *hist_k, const void *hist_v, const void *hist_q,
                              void *k_out, void *v_out, void *q_out, void *stream);
+
+/*
+ * Sequence-mixer operators that stand beside the memory: a short causal
+ * convolution with bias and activation, a selective state-space scan, and a
+ * group norm with activation, each with its gradients and (convolution and
+ * scan) its single-token form.
+ *
+ * Common to them:
+ *  - Tokens are [B, H, T, d] (batch, head, token, channel). Channels are
+ *    contiguous; the other strides are the caller's: `strides` is a host table
+ *    of three element strides (batch, head, token) for each strided tensor, in
+ *    the order that the entry point lists, or NULL when all of them are
+ *    contiguous. Strides are >= 0; an input may repeat rows (stride 0), an
+ *    output may not overlap itself. So a [B, T, H, d] tensor, or a slice of a
+ *    wider projection, is read and written where it lies.
+ *  - dtype is the type of the token tensors and their gradients (float32 or
+ *    bfloat16); parameters, states, statistics and their gradients are float32,
+ *    and all arithmetic is fp32, rounded once at the store. Parameters, states,
+ *    histories and statistics are contiguous.
+ *  - lengths: NULL, or device [B] int32, the tokens of each sequence of a padded
+ *    batch (values outside [0, T] are held to it). Rows behind a sequence's end
+ *    are not read; outputs there are left as they were, gradients of tokens
+ *    there are written as zeros. A sequence of length 0 is allowed.
+ *  - Pointers are aligned to their elements (workspaces to 256 bytes); wide
+ *    loads are used where bases, strides and sizes allow. d need not be a
+ *    multiple of anything.
+ *  - Outputs must not overlap inputs or one another (judged by the range from
+ *    first to last element), except state_end == state0 exactly in tm_scan.
+ *  - The calls are asynchronous on `stream` of the current device, allocate
+ *    nothing, can be captured into a graph, use no atomics (the same inputs
+ *    give the same bits), and hold no state between calls. A workspace belongs
+ *    to one call at a time: calls that may overlap on the GPU, captured graphs
+ *    included, need their own.
+ *  - Limits: H * d <= 2^24, B * H <= 2^24, B * H * d <= 2^31, d <= 2^20,
+ *    T < 2^30. TM_ERR_INVALID_ARG for bad arguments, TM_ERR_OOM for a
+ *    workspace that is too small, TM_ERR_UNSUPPORTED for a problem that needs
+ *    more than 2^31 - 1 thread blocks; none of these launches anything.
+ */
+
+/*
+ * Short depthwise causal convolution, per head h and channel c:
+ *   p[t] = bias[h, c] + sum_{j < width} filt[h, c, j] x[t - j],  y = act(p)
+ * the convolution of tm_prologue (same filter layout and history) with a bias,
+ * an activation and free strides, without the normalisation.
+ *
+ *   x, y       [B, H, T, d] dtype, strided (strides: x, y)
+ *   filt       [H, d, width]; bias [H, d] or NULL;  1 <= width <= 8
+ *   hist       [B, H, width-1, d] dtype or NULL: the tokens before the call, row
+ *              width-1+t holds token t < 0 (NULL = zeros)
+ *   tail       [B, H, width-1, d] dtype or NULL, output: the last width-1 tokens
+ *              of hist and x (of each sequence's own length): the next call's hist
+ */
+TM_API tm_status tm_conv(int B, int H, int T, int d, int width, tm_dtype dtype, tm_act act, const void *x,
+                         const float *filt, const float *bias, const void *hist, const int *lengths, void *y,
+                         void *tail, const long long *strides, void *stream);
+
+/*
+ * Gradients of sum <dy, y> + <dtail, tail> for the tm_conv call with these inputs.
+ *   dy [B, H, T, d] dtype, dtail like tail or NULL (= zeros)
+ *   dx [B, H, T, d] dtype, dfilt [H, d, width], dbias [H, d] or NULL,
+ *   dhist like hist or NULL                        outputs (strides: x, dy, dx)
+ */
+TM_API tm_status tm_conv_backward_workspace_size(int B, int H, int T, int d, int width, tm_dtype dtype, size_t *bytes);
+TM_API tm_status tm_conv_backward(int B, int H, int T, int d, int width, tm_dtype dtype, tm_act act, const void *x,
+                                  const float *filt, const float *bias, const void *hist, const int *lengths,
+                                  const void *dy, const void *dtail, void *dx, float *dfilt, float *dbias, void *dhist,
+                                  const long long *strides, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * One token per sequence: x, y [B, H, d] (strides: x, y; the token stride is
+ * not used), hist [B, H, width-1, d] moved on by the token in place. Same
+ * results as tm_conv with T = 1 and tail put back into hist.
+ */
+TM_API tm_status tm_conv_step(int B, int H, int d, int width, tm_dtype dtype, tm_act act, const void *x,
+                              const float *filt, const float *bias, void *hist, void *y, const long long *strides,
+                              void *stream);
+
+/*
+ * Selective state-space scan: N states per channel c of head h, whose decay
+ * and input depend on the token,
+ *   e_t = softplus(dt_t[c] + dt_bias[h, c])     (dt_softplus 0: without softplus)
+ *   h_t[c, n] = exp(e_t A[h, c, n]) h_{t-1}[c, n] + e_t x_t[c] Bm_t[n]
+ *   y_t[c] = sum_n Cm_t[n] h_t[c, n] + D[h, c] x_t[c],  times z_t[c] sigmoid(z_t[c])
+ *
+ *   x, dt, z, y  [B, H, T, d] dtype, strided; z may be NULL (no gate)
+ *   Bm, Cm       [B, G, T, N] dtype, strided: head h reads group h / (H / G)
+ *   A [H, d, N], D [H, d] or NULL, dt_bias [H, d] or NULL
+ *   state0, state_end [B, H, d, N] float32 or NULL: the state before the first
+ *                token (NULL = zeros) and after the last; they may be the same
+ *   strides      x, dt, Bm, Cm, z, y
+ * G divides H; 1 <= N <= 128. tm_scan_workspace_size may return 0 (workspace
+ * may then be NULL).
+ */
+TM_API tm_status tm_scan_workspace_size(int B, int H, int G, int T, int d, int N, tm_dtype dtype, size_t *bytes);
+TM_API tm_status tm_scan(int B, int H, int G, int T, int d, int N, tm_dtype dtype, int dt_softplus, const void *x,
+                         const void *dt, const float *A, const void *Bm, const void *Cm, const float *D, const void *z,
+                         const float *dt_bias, const float *state0, const int *lengths, void *y, float *state_end,
+                         const long long *strides, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Gradients of sum <dy, y> + <dstate_end, state_end> for the tm_scan call with
+ * these inputs; the forward is recomputed inside (the states at every 8th token
+ * are kept in the workspace).
+ *   dy [B, H, T, d] dtype; dstate_end [B, H, d, N] or NULL (= zeros)
+ *   dx, ddt, dz [B, H, T, d] dtype, strided (dz if and only if z);
+ *   dB, dC [B, G, T, N] dtype, contiguous, summed over the heads of a group;
+ *   dA [H, d, N]; dD, ddt_bias [H, d] or NULL; dstate0 [B, H, d, N] or NULL
+ *   strides      x, dt, Bm, Cm, z, dy, dx, ddt, dz
+ */
+TM_API tm_status tm_scan_backward_workspace_size(int B, int H, int G, int T, int d, int N, tm_dtype dtype,
+                                                 size_t *bytes);
+TM_API tm_status tm_scan_backward(int B, int H, int G, int T, int d, int N, tm_dtype dtype, int dt_softplus,
+                                  const void *x, const void *dt, const float *A, const void *Bm, const void *Cm,
+                                  const float *D, const void *z, const float *dt_bias, const float *state0,
+                                  const int *lengths, const void *dy, const float *dstate_end, void *dx, void *ddt,
+                                  float *dA, void *dB, void *dC, float *dD, void *dz, float *ddt_bias, float *dstate0,
+                                  const long long *strides, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * One token per sequence: x, dt, z, y [B, H, d], Bm, Cm [B, G, N] (strides as
+ * for tm_scan, the token strides are not used), state [B, H, d, N] updated in
+ * place: each of its values is read and written once. Same results as tm_scan
+ * with T = 1 and state_end == state0.
+ */
+TM_API tm_status tm_scan_step(int B, int H, int G, int d, int N, tm_dtype dtype, int dt_softplus, const void *x,
+                              const void *dt, const float *A, const void *Bm, const void *Cm, const float *D,
+                              const void *z, const float *dt_bias, float *state, void *y, const long long *strides,
+                              void *stream);
+
+/*
+ * Group norm with activation: the heads are the groups. With the mean and the
+ * (biased) variance over the d channels of one token (TM_NORM_TOKEN: the
+ * per-head norm of a memory's reads), or over the d channels of every token of
+ * the sequence (TM_NORM_SEQUENCE: group norm of a channels-last [B, T, H * d]
+ * tensor, whose heads are views with stride d),
+ *   p = weight[h, c] (x - mean) / sqrt(var + eps) + bias[h, c],  y = act(p)
+ *
+ *   x [B, H, T, d] in_dtype, y [B, H, T, d] out_dtype, strided (strides: x, y)
+ *   weight, bias [H, d] or NULL (= 1, 0)
+ *   stats [B, H, T, 2] (TM_NORM_TOKEN) or [B, H, 2], or NULL, output: mean and
+ *         1 / sqrt(var + eps) for the backward; zeros for an empty sequence, rows
+ *         behind a sequence's end left as they were; 8-byte aligned
+ *   workspace: tm_group_norm_workspace_size(..., backward = 0) bytes (may be 0)
+ */
+typedef enum { TM_NORM_TOKEN = 0, TM_NORM_SEQUENCE = 1 } tm_norm_over;
+TM_API tm_status tm_group_norm_workspace_size(int B, int H, int T, int d, tm_norm_over over, int backward,
+                                              size_t *bytes);
+TM_API tm_status tm_group_norm(int B, int H, int T, int d, tm_norm_over over, tm_dtype in_dtype, tm_dtype out_dtype,
+                               tm_act act, float eps, const void *x, const float *weight, const float *bias,
+                               const int *lengths, void *y, float *stats, const long long *strides, void *workspace,
+                               size_t workspace_bytes, void *stream);
+
+/*
+ * Gradients of sum <dy, y> for the tm_group_norm call with these inputs and
+ * the stats it wrote: dx [B, H, T, d] in_dtype (strides: x, dy, dx), dweight and
+ * dbias [H, d] or NULL. dy is out_dtype.
+ */
+TM_API tm_status tm_group_norm_backward(int B, int H, int T, int d, tm_norm_over over, tm_dtype in_dtype,
+                                        tm_dtype out_dtype, tm_act act, const void *x, const void *dy,
+                                        const float *stats, const float *weight, const float *bias, const int *lengths,
+                                        void *dx, float *dweight, float *dbias, const long long *strides,
+                                        void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * Test hook for failure handling (process-wide, host-only). inject_timeout != 0

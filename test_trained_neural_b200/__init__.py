@@ -5,3 +5,5 @@ this package is its thin Python binding.
 """
 from .memory import NeuralMemory, prologue  # noqa: F401
 from ._native import TitansMemError  # noqa: F401
+from .mixer import (group_norm, group_norm_backward, selective_scan, selective_scan_backward,  # noqa: F401
+                    selective_scan_step, short_conv, short_conv_backward, short_conv_step)

@@ -1,0 +1,784 @@
+// Group norm with an activation over tokens [B, H, T, d], the H groups of d
+// channels. Per group: mean m and variance over the d channels of one token
+// (kToken), or over the channels of every token of the sequence (kSequence);
+//   xh = (x - m) r, r = 1 / sqrt(var + eps),  p = weight xh + bias,  y = p or p sigmoid(p)
+// Gradients, with k = dy act'(p) weight and means over the same elements:
+//   dx = r (k - mean(k) - xh mean(k xh)),  dweight = sum dy act'(p) xh,  dbias = sum dy act'(p)
+// One token: a row's channels sit in the registers of LPR lanes, so x is read
+// once, and mean and variance are two passes over registers. A sequence: one
+// pass for the statistics (per-thread sums about the thread's first value,
+// joined as (count, mean, sum of squared differences)), one for the output.
+// Bound by HBM. The parameters' gradients leave each CTA as one partial and
+// are summed in a fixed order.
+#include "tm_mixer.cuh"
+
+namespace tmem {
+namespace mix {
+namespace {
+
+using bf16 = __nv_bfloat16;
+constexpr int NT = 256;
+
+template <int LPR>
+__device__ __forceinline__ float lanes_sum(float x) {
+#pragma unroll
+  for (int o = LPR / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+// Sum over a CTA of NT threads; `red` holds NT / 32 floats.
+__device__ __forceinline__ float cta_sum(float x, float *red) {
+  x = lanes_sum<32>(x);
+  __syncthreads();
+  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = x;
+  __syncthreads();
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < NT / 32; ++i) s += red[i];
+  return s;
+}
+__device__ __forceinline__ float act_grad(float p) {
+  const float q = sigmoid(p);
+  return q * fmaf(p, 1.f - q, 1.f);
+}
+
+// ---- one token
+
+// CTA: one (batch, head), NT / LPR rows side by side, RPT rows each.
+template <typename TI, typename TO, int V, int LPR, int IT, int RPT>
+__global__ void __launch_bounds__(NT) token_kernel(const Norm a, const int tiles) {
+  const int tile = blockIdx.x % tiles, bh = blockIdx.x / tiles;
+  const int h = bh % a.H, b = bh / a.H, d = a.d;
+  const int lane = threadIdx.x % LPR;
+  const int n = tokens_of(a.lengths, b, a.T);
+  const long long t0 = ((long long)tile * (NT / LPR) + threadIdx.x / LPR) * RPT;
+  const TI *x = static_cast<const TI *>(a.x) + b * a.sx.b + h * a.sx.h;
+  TO *y = static_cast<TO *>(a.y) + b * a.sy.b + h * a.sy.h;
+  Vec<TI, V> raw[RPT][IT];
+#pragma unroll
+  for (int r = 0; r < RPT; ++r)
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+      const int c = (i * LPR + lane) * V;
+      raw[r][i] = load_if<TI, V>(x + (t0 + r) * a.sx.t + c, c < d && t0 + r < n);
+    }
+  float w[IT][V], bs[IT][V];
+#pragma unroll
+  for (int i = 0; i < IT; ++i)
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const int c = (i * LPR + lane) * V + e;
+      w[i][e] = a.weight && c < d ? a.weight[(long long)h * d + c] : 1.f;
+      bs[i][e] = a.bias && c < d ? a.bias[(long long)h * d + c] : 0.f;
+    }
+  const float inv = 1.f / d;
+#pragma unroll
+  for (int r = 0; r < RPT; ++r) {
+    float m = 0.f, q = 0.f;
+#pragma unroll
+    for (int i = 0; i < IT; ++i)
+#pragma unroll
+      for (int e = 0; e < V; ++e) m += get(raw[r][i], e);        // lanes past d hold zeros
+    m = lanes_sum<LPR>(m) * inv;
+#pragma unroll
+    for (int i = 0; i < IT; ++i)
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float u = (i * LPR + lane) * V < d ? get(raw[r][i], e) - m : 0.f;
+        q = fmaf(u, u, q);
+      }
+    const float rs = rsqrtf(fmaf(lanes_sum<LPR>(q), inv, a.eps));
+    const long long t = t0 + r;
+    if (t >= n) continue;
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+      const int c = (i * LPR + lane) * V;
+      if (c >= d) continue;
+      Vec<TO, V> o;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float p = fmaf((get(raw[r][i], e) - m) * rs, w[i][e], bs[i][e]);
+        put(o, e, a.silu ? silu(p) : p);
+      }
+      store(y + t * a.sy.t + c, o);
+    }
+    if (a.stats && lane == 0) {
+      float2 *st = reinterpret_cast<float2 *>(a.stats) + ((long long)bh * a.T + t);
+      *st = make_float2(m, rs);
+    }
+  }
+}
+
+// Rows too long for registers: a CTA per row, which reads it three times (twice from L1 and L2).
+template <typename TI, typename TO>
+__global__ void __launch_bounds__(NT) token_wide_kernel(const Norm a) {
+  __shared__ float red[NT / 32];
+  const long long row = blockIdx.x;
+  const int t = (int)(row % a.T), bh = (int)(row / a.T);
+  const int h = bh % a.H, b = bh / a.H, d = a.d;
+  if (t >= tokens_of(a.lengths, b, a.T)) return;
+  const TI *x = static_cast<const TI *>(a.x) + b * a.sx.b + h * a.sx.h + t * a.sx.t;
+  TO *y = static_cast<TO *>(a.y) + b * a.sy.b + h * a.sy.h + t * a.sy.t;
+  float m = 0.f, q = 0.f;
+  for (int c = threadIdx.x; c < d; c += NT) m += to_f(x[c]);
+  m = cta_sum(m, red) / d;
+  for (int c = threadIdx.x; c < d; c += NT) {
+    const float u = to_f(x[c]) - m;
+    q = fmaf(u, u, q);
+  }
+  const float rs = rsqrtf(cta_sum(q, red) / d + a.eps);
+  for (int c = threadIdx.x; c < d; c += NT) {
+    const long long hc = (long long)h * d + c;
+    const float p = fmaf((to_f(x[c]) - m) * rs, a.weight ? a.weight[hc] : 1.f, a.bias ? a.bias[hc] : 0.f);
+    Vec<TO, 1> o;
+    put(o, 0, a.silu ? silu(p) : p);
+    y[c] = o.e[0];
+  }
+  if (a.stats && threadIdx.x == 0) reinterpret_cast<float2 *>(a.stats)[(long long)bh * a.T + t] = make_float2(m, rs);
+}
+
+// CTA: one (batch, head) and the rows tile, tile + tiles, ... in steps of
+// NT / LPR; the lane's channels are fixed, so the parameters' gradients are
+// summed in registers over all rows of the CTA.
+template <typename TI, typename TO, int V, int LPR, int IT, int RPT>
+__global__ void __launch_bounds__(NT) token_backward_kernel(const Norm a, const int tiles, float *part) {
+  extern __shared__ float red[];                        // [NT][V]
+  const int tile = blockIdx.x % tiles, bh = blockIdx.x / tiles;
+  const int h = bh % a.H, b = bh / a.H, d = a.d;
+  const int lane = threadIdx.x % LPR, rg = threadIdx.x / LPR;
+  constexpr int ROWS = NT / LPR;
+  const int n = tokens_of(a.lengths, b, a.T);
+  const TI *x = static_cast<const TI *>(a.x) + b * a.sx.b + h * a.sx.h;
+  const TO *dy = static_cast<const TO *>(a.dy) + b * a.sdy.b + h * a.sdy.h;
+  TI *dx = static_cast<TI *>(a.dx) + b * a.sdx.b + h * a.sdx.h;
+  const float2 *stats = reinterpret_cast<const float2 *>(a.stats) + (long long)bh * a.T;
+  float w[IT][V], bs[IT][V], dw[IT][V], db[IT][V];
+#pragma unroll
+  for (int i = 0; i < IT; ++i)
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const int c = (i * LPR + lane) * V + e;
+      w[i][e] = a.weight && c < d ? a.weight[(long long)h * d + c] : 1.f;
+      bs[i][e] = a.bias && c < d ? a.bias[(long long)h * d + c] : 0.f;
+      dw[i][e] = db[i][e] = 0.f;
+    }
+  const float inv = 1.f / d;
+  const long long step = (long long)tiles * ROWS * RPT;
+  for (long long tb = (long long)tile * ROWS * RPT; tb < a.T; tb += step) {
+    Vec<TI, V> xr[RPT][IT];
+    Vec<TO, V> yr[RPT][IT];
+    float2 st[RPT];
+#pragma unroll
+    for (int r = 0; r < RPT; ++r) {
+      const long long t = tb + r * ROWS + rg;
+      st[r] = t < n ? stats[t] : make_float2(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < IT; ++i) {
+        const int c = (i * LPR + lane) * V;
+        xr[r][i] = load_if<TI, V>(x + t * a.sx.t + c, c < d && t < n);
+        yr[r][i] = load_if<TO, V>(dy + t * a.sdy.t + c, c < d && t < n);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < RPT; ++r) {
+      const long long t = tb + r * ROWS + rg;
+      const float m = st[r].x, rs = st[r].y;
+      float k[IT][V], k1 = 0.f, k2 = 0.f;
+#pragma unroll
+      for (int i = 0; i < IT; ++i)
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const float xh = (get(xr[r][i], e) - m) * rs;
+          float q = get(yr[r][i], e);                    // zero past d and past the sequence
+          if (a.silu) q *= act_grad(fmaf(xh, w[i][e], bs[i][e]));
+          db[i][e] += q;
+          dw[i][e] = fmaf(q, xh, dw[i][e]);
+          k[i][e] = q * w[i][e];
+          k1 += k[i][e];
+          k2 = fmaf(k[i][e], xh, k2);
+        }
+      k1 = lanes_sum<LPR>(k1) * inv;
+      k2 = lanes_sum<LPR>(k2) * inv;
+      if (t >= a.T) continue;
+#pragma unroll
+      for (int i = 0; i < IT; ++i) {
+        const int c = (i * LPR + lane) * V;
+        if (c >= d) continue;
+        Vec<TI, V> o;
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const float xh = (get(xr[r][i], e) - m) * rs;
+          put(o, e, t < n ? rs * (k[i][e] - k1 - xh * k2) : 0.f);
+        }
+        store(dx + t * a.sdx.t + c, o);
+      }
+    }
+  }
+  // partial of the CTA: [b, tile][2][h, c]
+  float *out = part + ((long long)b * tiles + tile) * 2 * a.H * d + (long long)h * d;
+#pragma unroll
+  for (int i = 0; i < IT; ++i)
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) red[threadIdx.x * V + e] = p ? db[i][e] : dw[i][e];
+      __syncthreads();
+      const int c = (i * LPR + lane) * V;
+      if (rg == 0 && c < d)
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          float s = 0.f;
+          for (int q = 0; q < ROWS; ++q) s += red[(q * LPR + lane) * V + e];
+          out[(long long)p * a.H * d + c + e] = s;
+        }
+      __syncthreads();
+    }
+}
+
+// Rows too long for registers: a CTA walks rows of one (batch, head); the
+// parameters' gradients are summed in its own partial in global memory.
+template <typename TI, typename TO>
+__global__ void __launch_bounds__(NT) token_wide_backward_kernel(const Norm a, const int tiles, float *part) {
+  __shared__ float red[NT / 32];
+  const int tile = blockIdx.x % tiles, bh = blockIdx.x / tiles;
+  const int h = bh % a.H, b = bh / a.H, d = a.d;
+  const int n = tokens_of(a.lengths, b, a.T);
+  float *out = part + ((long long)b * tiles + tile) * 2 * a.H * d + (long long)h * d;
+  float *out2 = out + (long long)a.H * d;
+  for (int c = threadIdx.x; c < d; c += NT) out[c] = out2[c] = 0.f;
+  for (int t = tile; t < a.T; t += tiles) {
+    TI *dx = static_cast<TI *>(a.dx) + b * a.sdx.b + h * a.sdx.h + t * a.sdx.t;
+    const TI *x = static_cast<const TI *>(a.x) + b * a.sx.b + h * a.sx.h + t * a.sx.t;
+    const TO *dy = static_cast<const TO *>(a.dy) + b * a.sdy.b + h * a.sdy.h + t * a.sdy.t;
+    Vec<TI, 1> o;
+    if (t >= n) {
+      put(o, 0, 0.f);
+      for (int c = threadIdx.x; c < d; c += NT) dx[c] = o.e[0];
+      continue;
+    }
+    const float2 st = reinterpret_cast<const float2 *>(a.stats)[(long long)bh * a.T + t];
+    float k1 = 0.f, k2 = 0.f;
+    for (int c = threadIdx.x; c < d; c += NT) {
+      const long long hc = (long long)h * d + c;
+      const float w = a.weight ? a.weight[hc] : 1.f, xh = (to_f(x[c]) - st.x) * st.y;
+      float q = to_f(dy[c]);
+      if (a.silu) q *= act_grad(fmaf(xh, w, a.bias ? a.bias[hc] : 0.f));
+      out[c] = fmaf(q, xh, out[c]);
+      out2[c] += q;
+      k1 = fmaf(q, w, k1);
+      k2 = fmaf(q * w, xh, k2);
+    }
+    k1 = cta_sum(k1, red) / d;
+    k2 = cta_sum(k2, red) / d;
+    for (int c = threadIdx.x; c < d; c += NT) {
+      const long long hc = (long long)h * d + c;
+      const float w = a.weight ? a.weight[hc] : 1.f, xh = (to_f(x[c]) - st.x) * st.y;
+      float q = to_f(dy[c]);
+      if (a.silu) q *= act_grad(fmaf(xh, w, a.bias ? a.bias[hc] : 0.f));
+      put(o, 0, st.y * (fmaf(q, w, -k1) - xh * k2));
+      dx[c] = o.e[0];
+    }
+  }
+}
+
+// ---- a sequence. Heads next to one another in every token row are walked as
+// one row of W = H d channels ("joined"); a thread owns V channels of one head.
+
+struct Cols {
+  int joined;        // W = H d and one unit per batch entry, or W = d and one per (batch, head)
+  int W, nv, nvb, cb, RL, tiles, run;
+};
+Cols cols_of(int B, int H, int T, int d, int V, bool joined) {
+  Cols s;
+  s.joined = joined;
+  s.W = joined ? H * d : d;
+  s.nv = s.W / V;
+  s.nvb = s.nv < 64 ? s.nv : 64;
+  s.cb = (s.nv + s.nvb - 1) / s.nvb;
+  s.RL = NT / s.nvb;
+  const long long units = (long long)B * (joined ? 1 : H) * s.cb;
+  s.run = 64;
+  while (s.run > 8 && units * ((T + (long long)s.run * s.RL - 1) / ((long long)s.run * s.RL)) < kSMs * 8) s.run /= 2;
+  s.tiles = (int)((T + (long long)s.run * s.RL - 1) / ((long long)s.run * s.RL));
+  return s;
+}
+struct At {
+  int b, h0, v, c, tile, rl, vi;     // batch, first head of the unit, vector, channel in the unit, ...
+  bool mine;
+};
+__device__ __forceinline__ At at_of(const Norm &a, const Cols &s, int V) {
+  At q;
+  unsigned blk = blockIdx.x;
+  q.tile = blk % s.tiles;
+  blk /= s.tiles;
+  const int cb = blk % s.cb;
+  blk /= s.cb;
+  q.h0 = s.joined ? 0 : blk % a.H;
+  q.b = s.joined ? blk : blk / a.H;
+  q.vi = threadIdx.x % s.nvb;
+  q.rl = threadIdx.x / s.nvb;
+  q.v = cb * s.nvb + q.vi;
+  q.mine = q.v < s.nv && q.rl < s.RL;
+  q.c = q.v * V;
+  return q;
+}
+
+// Statistics: (count, mean, sum of squares about the mean) of each vector
+// column and row tile, [b][tile][H d / V].
+template <typename TI, int V>
+__global__ void __launch_bounds__(NT) seq_stats_kernel(const Norm a, const Cols s, float2 *part) {
+  __shared__ float3 red[NT];
+  const At q = at_of(a, s, V);
+  const int n = tokens_of(a.lengths, q.b, a.T);
+  float3 mine = make_float3(0.f, 0.f, 0.f);
+  if (q.mine) {
+    const TI *x = static_cast<const TI *>(a.x) + q.b * a.sx.b + q.h0 * a.sx.h + q.c;
+    const long long t0 = ((long long)q.tile * s.RL + q.rl) * s.run;
+    const long long t1 = t0 + s.run < n ? t0 + s.run : n;
+    if (t0 < t1) {
+      float k = 0.f, s1 = 0.f, s2 = 0.f;
+      for (long long t = t0; t < t1; t += 8) {
+        Vec<TI, V> raw[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) raw[i] = load_if<TI, V>(x + (t + i) * a.sx.t, t + i < t1);
+        if (t == t0) k = get(raw[0], 0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (t + i < t1)
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+              const float u = get(raw[i], e) - k;
+              s1 += u;
+              s2 = fmaf(u, u, s2);
+            }
+      }
+      const float cnt = (float)((t1 - t0) * V), mean = s1 / cnt;
+      mine = make_float3(cnt, k + mean, fmaxf(s2 - s1 * mean, 0.f));
+    }
+  }
+  red[threadIdx.x] = mine;
+  __syncthreads();
+  if (q.rl || !q.mine) return;
+  float3 t = red[threadIdx.x];
+  for (int r = 1; r < s.RL; ++r) {
+    const float3 o = red[r * s.nvb + q.vi];
+    if (o.x == 0.f) continue;
+    const float nn = t.x + o.x, dm = o.y - t.y, f = o.x / nn;
+    t.z += o.z + dm * dm * t.x * f;
+    t.y += dm * f;
+    t.x = nn;
+  }
+  const long long vecs = (long long)a.H * a.d / V;
+  part[((long long)q.b * s.tiles + q.tile) * vecs + q.h0 * (a.d / V) + q.v] = make_float2(t.y, t.z);
+}
+
+// Joins the partials of one (batch, head), in 64 bits, in a fixed order.
+__global__ void __launch_bounds__(NT) seq_join_kernel(const Norm a, const Cols s, const int V, const float2 *part,
+                                                      float2 *stats) {
+  __shared__ double red[3][NT / 32];
+  const int bh = blockIdx.x, h = bh % a.H, b = bh / a.H;
+  const int n = tokens_of(a.lengths, b, a.T);
+  const int vh = a.d / V;
+  const long long vecs = (long long)a.H * vh, total = (long long)s.tiles * vh;
+  const long long span = (long long)s.run * s.RL;
+  auto count = [&](long long i) {
+    const long long left = n - (i / vh) * span;
+    return (double)((left < 0 ? 0 : left < span ? left : span) * V);
+  };
+  auto entry = [&](long long i) { return part[((long long)b * s.tiles + i / vh) * vecs + (long long)h * vh + i % vh]; };
+  auto all = [&](double x, int k) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    if (threadIdx.x % 32 == 0) red[k][threadIdx.x / 32] = x;
+    __syncthreads();
+    double y = 0.;
+#pragma unroll
+    for (int i = 0; i < NT / 32; ++i) y += red[k][i];
+    return y;
+  };
+  const double cnt = (double)n * a.d;
+  double s1 = 0., s2 = 0.;
+  for (long long i = threadIdx.x; i < total; i += NT) {
+    const double k = count(i);
+    if (k > 0.) s1 += k * entry(i).x;
+  }
+  const double mean = cnt > 0. ? all(s1, 0) / cnt : 0.;
+  for (long long i = threadIdx.x; i < total; i += NT) {
+    const double k = count(i);
+    if (k > 0.) {
+      const float2 e = entry(i);
+      s2 += e.y + k * (e.x - mean) * (e.x - mean);
+    }
+  }
+  s2 = all(s2, 1);
+  if (threadIdx.x == 0)
+    stats[bh] = n > 0 ? make_float2((float)mean, (float)(1. / sqrt(s2 / cnt + (double)a.eps))) : make_float2(0.f, 0.f);
+}
+
+template <typename TI, typename TO, int V>
+__global__ void __launch_bounds__(NT) seq_apply_kernel(const Norm a, const Cols s, const float2 *stats) {
+  const At q = at_of(a, s, V);
+  if (!q.mine) return;
+  const int n = tokens_of(a.lengths, q.b, a.T);
+  const int h = q.h0 + q.c / a.d;
+  const TI *x = static_cast<const TI *>(a.x) + q.b * a.sx.b + q.h0 * a.sx.h + q.c;
+  TO *y = static_cast<TO *>(a.y) + q.b * a.sy.b + q.h0 * a.sy.h + q.c;
+  const float2 st = stats[(long long)q.b * a.H + h];
+  const long long hc = (long long)q.h0 * a.d + q.c;
+  float w[V], bs[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    w[e] = a.weight ? a.weight[hc + e] : 1.f;
+    bs[e] = a.bias ? a.bias[hc + e] : 0.f;
+  }
+  const long long t0 = ((long long)q.tile * s.RL + q.rl) * s.run;
+  const long long t1 = t0 + s.run < n ? t0 + s.run : n;
+  for (long long t = t0; t < t1; t += 4) {
+    Vec<TI, V> raw[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) raw[i] = load_if<TI, V>(x + (t + i) * a.sx.t, t + i < t1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      Vec<TO, V> o;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float p = fmaf((get(raw[i], e) - st.x) * st.y, w[e], bs[e]);
+        put(o, e, a.silu ? silu(p) : p);
+      }
+      if (t + i < t1) store(y + (t + i) * a.sy.t, o);
+    }
+  }
+}
+
+// Per channel the sums of dy act'(p) xh and dy act'(p) over a row tile: [b, tile][2][h, c].
+template <typename TI, typename TO, int V>
+__global__ void __launch_bounds__(NT) seq_sums_kernel(const Norm a, const Cols s, float *part) {
+  __shared__ float red[NT * V];
+  const At q = at_of(a, s, V);
+  const int n = tokens_of(a.lengths, q.b, a.T);
+  float dw[V], db[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) dw[e] = db[e] = 0.f;
+  const long long hc = (long long)q.h0 * a.d + q.c;
+  if (q.mine) {
+    const int h = q.h0 + q.c / a.d;
+    const TI *x = static_cast<const TI *>(a.x) + q.b * a.sx.b + q.h0 * a.sx.h + q.c;
+    const TO *dy = static_cast<const TO *>(a.dy) + q.b * a.sdy.b + q.h0 * a.sdy.h + q.c;
+    const float2 st = reinterpret_cast<const float2 *>(a.stats)[(long long)q.b * a.H + h];
+    float w[V], bs[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      w[e] = a.weight ? a.weight[hc + e] : 1.f;
+      bs[e] = a.bias ? a.bias[hc + e] : 0.f;
+    }
+    const long long t0 = ((long long)q.tile * s.RL + q.rl) * s.run;
+    const long long t1 = t0 + s.run < n ? t0 + s.run : n;
+    for (long long t = t0; t < t1; t += 4) {
+      Vec<TI, V> xr[4];
+      Vec<TO, V> yr[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        xr[i] = load_if<TI, V>(x + (t + i) * a.sx.t, t + i < t1);
+        yr[i] = load_if<TO, V>(dy + (t + i) * a.sdy.t, t + i < t1);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const float xh = (get(xr[i], e) - st.x) * st.y;
+          float k = get(yr[i], e);
+          if (a.silu) k *= act_grad(fmaf(xh, w[e], bs[e]));
+          if (t + i < t1) {
+            db[e] += k;
+            dw[e] = fmaf(k, xh, dw[e]);
+          }
+        }
+    }
+  }
+  float *out = part + ((long long)q.b * s.tiles + q.tile) * 2 * a.H * a.d + hc;
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) red[threadIdx.x * V + e] = p ? db[e] : dw[e];
+    __syncthreads();
+    if (q.rl == 0 && q.mine)
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        float t = 0.f;
+        for (int r = 0; r < s.RL; ++r) t += red[(r * s.nvb + q.vi) * V + e];
+        out[(long long)p * a.H * a.d + e] = t;
+      }
+    __syncthreads();
+  }
+}
+
+// Sums of one (batch, head): per channel over the row tiles, [b][2][h, c], and
+// the means of k and k xh over the group.
+__global__ void __launch_bounds__(NT) seq_join_sums_kernel(const Norm a, const int tiles, const float *part, float *chan,
+                                                           float2 *means) {
+  __shared__ float slice[2][8][32];
+  __shared__ float tot[2][32];
+  const int bh = blockIdx.x, h = bh % a.H, b = bh / a.H, d = a.d;
+  const long long hd = (long long)a.H * d;
+  const int l = threadIdx.x % 32, k = threadIdx.x / 32;
+  float k1 = 0.f, k2 = 0.f;
+  for (int c0 = 0; c0 < d; c0 += 32) {
+    const int c = c0 + l;
+    float dw = 0.f, db = 0.f;
+    if (c < d)
+      for (int t = k; t < tiles; t += 8) {
+        const float *p = part + ((long long)b * tiles + t) * 2 * hd + (long long)h * d + c;
+        dw += p[0];
+        db += p[hd];
+      }
+    slice[0][k][l] = dw;
+    slice[1][k][l] = db;
+    __syncthreads();
+    if (k == 0 && c < d) {
+      dw = db = 0.f;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        dw += slice[0][q][l];
+        db += slice[1][q][l];
+      }
+      float *o = chan + (long long)b * 2 * hd + (long long)h * d + c;
+      o[0] = dw;
+      o[hd] = db;
+      const float w = a.weight ? a.weight[(long long)h * d + c] : 1.f;
+      k1 = fmaf(w, db, k1);
+      k2 = fmaf(w, dw, k2);
+    }
+    __syncthreads();
+  }
+  if (k) return;
+  tot[0][l] = k1;
+  tot[1][l] = k2;
+  __syncwarp();
+  if (l) return;
+  k1 = k2 = 0.f;
+  for (int i = 0; i < 32; ++i) {
+    k1 += tot[0][i];
+    k2 += tot[1][i];
+  }
+  const int n = tokens_of(a.lengths, b, a.T);
+  const float cnt = n > 0 ? (float)n * d : 1.f;
+  means[bh] = make_float2(k1 / cnt, k2 / cnt);
+}
+
+template <typename TI, typename TO, int V>
+__global__ void __launch_bounds__(NT) seq_grad_kernel(const Norm a, const Cols s, const float2 *means) {
+  const At q = at_of(a, s, V);
+  if (!q.mine) return;
+  const int n = tokens_of(a.lengths, q.b, a.T);
+  const int h = q.h0 + q.c / a.d;
+  const TI *x = static_cast<const TI *>(a.x) + q.b * a.sx.b + q.h0 * a.sx.h + q.c;
+  const TO *dy = static_cast<const TO *>(a.dy) + q.b * a.sdy.b + q.h0 * a.sdy.h + q.c;
+  TI *dx = static_cast<TI *>(a.dx) + q.b * a.sdx.b + q.h0 * a.sdx.h + q.c;
+  const float2 st = reinterpret_cast<const float2 *>(a.stats)[(long long)q.b * a.H + h];
+  const float2 mk = means[(long long)q.b * a.H + h];
+  const long long hc = (long long)q.h0 * a.d + q.c;
+  float w[V], bs[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    w[e] = a.weight ? a.weight[hc + e] : 1.f;
+    bs[e] = a.bias ? a.bias[hc + e] : 0.f;
+  }
+  const long long t0 = ((long long)q.tile * s.RL + q.rl) * s.run;
+  const long long t1 = t0 + s.run < a.T ? t0 + s.run : a.T;
+  for (long long t = t0; t < t1; t += 4) {
+    Vec<TI, V> xr[4];
+    Vec<TO, V> yr[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool live = t + i < t1 && t + i < n;
+      xr[i] = load_if<TI, V>(x + (t + i) * a.sx.t, live);
+      yr[i] = load_if<TO, V>(dy + (t + i) * a.sdy.t, live);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      Vec<TI, V> o;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float xh = (get(xr[i], e) - st.x) * st.y;
+        float k = get(yr[i], e);
+        if (a.silu) k *= act_grad(fmaf(xh, w[e], bs[e]));
+        put(o, e, t + i < n ? st.y * (fmaf(k, w[e], -mk.x) - xh * mk.y) : 0.f);
+      }
+      if (t + i < t1) store(dx + (t + i) * a.sdx.t, o);
+    }
+  }
+}
+
+// out = sum of n-vectors; dweight first, then dbias (either may be absent).
+__global__ void __launch_bounds__(256) pair_sum_kernel(const float *part, int parts, long long hd, float *dweight,
+                                                       float *dbias) {
+  __shared__ float red[8][32];
+  const long long n = 2 * hd, i = (long long)blockIdx.x * 32 + threadIdx.x % 32;
+  const int k = threadIdx.x / 32;
+  float s = 0.f;
+  if (i < n)
+    for (int p = k; p < parts; p += 8) s += part[p * n + i];
+  red[k][threadIdx.x % 32] = s;
+  __syncthreads();
+  if (k || i >= n) return;
+  s = 0.f;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) s += red[q][threadIdx.x];
+  if (i < hd) {
+    if (dweight) dweight[i] = s;
+  } else if (dbias) {
+    dbias[i - hd] = s;
+  }
+}
+cudaError_t pair_sum(const float *part, int parts, long long hd, float *dweight, float *dbias, cudaStream_t st) {
+  if (!dweight && !dbias) return cudaSuccess;
+  pair_sum_kernel<<<(unsigned)((2 * hd + 31) / 32), 256, 0, st>>>(part, parts, hd, dweight, dbias);
+  return cudaGetLastError();
+}
+
+// CTAs of a (batch, head) that share its rows in the token-wise backward:
+// enough to fill the GPU a few times over, each with rows to sum over.
+int token_tiles(int B, int H, int T, int d) {
+  const long long bh = (long long)B * H;
+  long long tiles = ((long long)kSMs * 8 + bh - 1) / bh;
+  const long long most = ((long long)T + 31) / 32;
+  if (tiles > most) tiles = most;
+  return (int)(tiles < 1 ? 1 : tiles);
+}
+
+template <typename TI, typename TO>
+cudaError_t forward(const Norm &a, cudaStream_t st) {
+  constexpr int V = sizeof(TI) == 2 ? 8 : 4;
+  const int ei = sizeof(TI), eo = sizeof(TO);
+  const bool vec = fits(a.x, a.sx, a.d, V, ei) && fits(a.y, a.sy, a.d, V, eo);
+  const long long bh = (long long)a.B * a.H;
+  if (a.over == kToken) {
+    auto go = [&](auto kern, int LPR, int RPT) {
+      const long long rows = (long long)NT / LPR * RPT, tiles = (a.T + rows - 1) / rows;
+      if (bh * tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
+      kern<<<(unsigned)(bh * tiles), NT, 0, st>>>(a, (int)tiles);
+      return cudaGetLastError();
+    };
+    if (vec) {
+      if (a.d <= 8 * V) return go(token_kernel<TI, TO, V, 8, 1, 4>, 8, 4);
+      if (a.d <= 16 * V) return go(token_kernel<TI, TO, V, 16, 1, 4>, 16, 4);
+      if (a.d <= 32 * V) return go(token_kernel<TI, TO, V, 32, 1, 4>, 32, 4);
+      if (a.d <= 64 * V) return go(token_kernel<TI, TO, V, 32, 2, 2>, 32, 2);
+      if (a.d <= 128 * V) return go(token_kernel<TI, TO, V, 32, 4, 1>, 32, 1);
+    }
+    if (a.d <= 32) return go(token_kernel<TI, TO, 1, 32, 1, 4>, 32, 4);
+    if (a.d <= 256) return go(token_kernel<TI, TO, 1, 32, 8, 1>, 32, 1);
+    if (bh * a.T > 0x7fffffffLL) return cudaErrorInvalidValue;
+    token_wide_kernel<TI, TO><<<(unsigned)(bh * a.T), NT, 0, st>>>(a);
+    return cudaGetLastError();
+  }
+  const bool joined = a.H > 1 && a.sx.h == a.d && a.sy.h == a.d;
+  auto go = [&](auto stats, auto apply, int VV) {
+    const Cols s = cols_of(a.B, a.H, a.T, a.d, VV, joined);
+    const long long grid = (long long)a.B * (joined ? 1 : a.H) * s.cb * s.tiles;
+    if (grid > 0x7fffffffLL || bh > 0x7fffffffLL) return cudaErrorInvalidValue;
+    float2 *part = static_cast<float2 *>(a.ws);
+    float2 *st2 = a.stats ? reinterpret_cast<float2 *>(a.stats) : part + (size_t)a.B * s.tiles * a.H * (a.d / VV);
+    const int threads = NT;
+    stats<<<(unsigned)grid, threads, 0, st>>>(a, s, part);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    seq_join_kernel<<<(unsigned)bh, NT, 0, st>>>(a, s, VV, part, st2);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    apply<<<(unsigned)grid, threads, 0, st>>>(a, s, st2);
+    return cudaGetLastError();
+  };
+  if (vec) return go(seq_stats_kernel<TI, V>, seq_apply_kernel<TI, TO, V>, V);
+  return go(seq_stats_kernel<TI, 1>, seq_apply_kernel<TI, TO, 1>, 1);
+}
+
+template <typename TI, typename TO>
+cudaError_t backward(const Norm &a, cudaStream_t st) {
+  constexpr int V = sizeof(TI) == 2 ? 8 : 4;
+  const int ei = sizeof(TI), eo = sizeof(TO);
+  const bool vec = fits(a.x, a.sx, a.d, V, ei) && fits(a.dx, a.sdx, a.d, V, ei) && fits(a.dy, a.sdy, a.d, V, eo);
+  const long long bh = (long long)a.B * a.H, hd = (long long)a.H * a.d;
+  float *part = static_cast<float *>(a.ws);
+  if (a.over == kToken) {
+    const int tiles = token_tiles(a.B, a.H, a.T, a.d);
+    if (bh * tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
+    auto go = [&](auto kern, int VV) {
+      kern<<<(unsigned)(bh * tiles), NT, NT * VV * sizeof(float), st>>>(a, tiles, part);
+      const cudaError_t e = cudaGetLastError();
+      return e != cudaSuccess ? e : pair_sum(part, a.B * tiles, hd, a.dweight, a.dbias, st);
+    };
+    if (vec) {
+      if (a.d <= 8 * V) return go(token_backward_kernel<TI, TO, V, 8, 1, 2>, V);
+      if (a.d <= 16 * V) return go(token_backward_kernel<TI, TO, V, 16, 1, 2>, V);
+      if (a.d <= 32 * V) return go(token_backward_kernel<TI, TO, V, 32, 1, 2>, V);
+      if (a.d <= 64 * V) return go(token_backward_kernel<TI, TO, V, 32, 2, 1>, V);
+      if (V == 4 && a.d <= 128 * V) return go(token_backward_kernel<TI, TO, V, 32, 4, 1>, V);
+    }
+    if (a.d <= 32) return go(token_backward_kernel<TI, TO, 1, 32, 1, 2>, 1);
+    if (a.d <= 256) return go(token_backward_kernel<TI, TO, 1, 32, 8, 1>, 1);
+    token_wide_backward_kernel<TI, TO><<<(unsigned)(bh * tiles), NT, 0, st>>>(a, tiles, part);
+    const cudaError_t e = cudaGetLastError();
+    return e != cudaSuccess ? e : pair_sum(part, a.B * tiles, hd, a.dweight, a.dbias, st);
+  }
+  const bool joined = a.H > 1 && a.sx.h == a.d && a.sdy.h == a.d && a.sdx.h == a.d;
+  auto go = [&](auto sums, auto grad, int VV) {
+    const Cols s = cols_of(a.B, a.H, a.T, a.d, VV, joined);
+    const long long grid = (long long)a.B * (joined ? 1 : a.H) * s.cb * s.tiles;
+    if (grid > 0x7fffffffLL || bh > 0x7fffffffLL) return cudaErrorInvalidValue;
+    float *chan = part + (size_t)a.B * s.tiles * 2 * hd;
+    float2 *means = reinterpret_cast<float2 *>(chan + (size_t)a.B * 2 * hd);
+    sums<<<(unsigned)grid, NT, 0, st>>>(a, s, part);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    seq_join_sums_kernel<<<(unsigned)bh, NT, 0, st>>>(a, s.tiles, part, chan, means);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    grad<<<(unsigned)grid, NT, 0, st>>>(a, s, means);
+    e = cudaGetLastError();
+    return e != cudaSuccess ? e : pair_sum(chan, a.B, hd, a.dweight, a.dbias, st);
+  };
+  if (vec) return go(seq_sums_kernel<TI, TO, V>, seq_grad_kernel<TI, TO, V>, V);
+  return go(seq_sums_kernel<TI, TO, 1>, seq_grad_kernel<TI, TO, 1>, 1);
+}
+
+}  // namespace
+
+// Statistics' partials: the largest over the vector widths and the joining of
+// heads that the launch may choose.
+size_t norm_ws(int B, int H, int T, int d, Over over) {
+  if (over == kToken) return 0;
+  size_t most = 0;
+  for (const int V : {1, 4, 8})
+    for (const bool joined : {false, true}) {
+      if (d % V) continue;
+      const size_t n = (size_t)B * cols_of(B, H, T, d, V, joined).tiles * H * (d / V) + (size_t)B * H;
+      if (n > most) most = n;
+    }
+  return up256(most * 8);
+}
+
+size_t norm_backward_ws(int B, int H, int T, int d, Over over) {
+  const size_t hd = (size_t)H * d;
+  if (over == kToken) return up256((size_t)B * token_tiles(B, H, T, d) * 2 * hd * 4);
+  size_t tiles = 0;
+  for (const int V : {1, 4, 8})
+    for (const bool joined : {false, true}) {
+      if (d % V) continue;
+      const size_t n = cols_of(B, H, T, d, V, joined).tiles;
+      if (n > tiles) tiles = n;
+    }
+  return up256(((size_t)B * (tiles + 1) * 2 * hd + 2 * (size_t)B * H) * 4);
+}
+
+cudaError_t norm_launch(Norm a, cudaStream_t st) {
+  if (a.in_bf16) return a.out_bf16 ? forward<bf16, bf16>(a, st) : forward<bf16, float>(a, st);
+  return a.out_bf16 ? forward<float, bf16>(a, st) : forward<float, float>(a, st);
+}
+
+cudaError_t norm_backward_launch(Norm a, cudaStream_t st) {
+  if (a.in_bf16) return a.out_bf16 ? backward<bf16, bf16>(a, st) : backward<bf16, float>(a, st);
+  return a.out_bf16 ? backward<float, bf16>(a, st) : backward<float, float>(a, st);
+}
+
+}  // namespace mix
+}  // namespace tmem

@@ -1,0 +1,90 @@
+// What the forward and backward of the selective scan share.
+//
+// The recurrence, per (batch, head), channel c and state n:
+//   e = softplus(dt + dt_bias)      (or dt + dt_bias)
+//   h_t[c, n] = exp(e A[c, n]) h_{t-1}[c, n] + e x_t[c] Bm_t[n]
+//   y_t[c] = (sum_n Cm_t[n] h_t[c, n] + D[c] x_t[c]) z sigmoid(z)
+//
+// Layout of the work: NL lanes share a channel, each with 4 consecutive
+// states (N <= 4 NL, the rest padded with A = B = C = 0, which leaves them
+// zero), and a lane owns CPL channels, so a warp covers 32 / NL * CPL channels
+// and a lane's B_t and C_t are one 16-byte shared-memory load each for
+// 4 CPL state updates. Sums over the states of a channel end with a few
+// shuffles in which the lanes exchange halves of their channels.
+#pragma once
+#include "tm_mixer.cuh"
+
+namespace tmem {
+namespace mix {
+
+constexpr int SPL = 4;               // states a lane holds of each of its channels
+
+// Sum of M values per lane over NL lanes that are STEP apart: at each step a
+// lane passes on half of its values and adds what it gets to the other half,
+// so a value costs about one shuffle. Afterwards lane number nl of them holds
+// the totals of the values first(nl) .. first(nl) + kept - 1 in v[0 ..]
+// (when NL > M, lanes that agree in their low log2(M) bits hold the same one).
+template <int M, int NL, int STEP = 1>
+struct LaneSum {
+  static constexpr int kept = M >= NL ? M / NL : 1;
+  static constexpr int writers = M < NL ? M : NL;      // lanes below this number hold every total once
+  __device__ static __forceinline__ void run(float (&v)[M], int nl) {
+    int m = M;
+#pragma unroll
+    for (int bit = 1; bit < NL; bit *= 2) {
+      if (m > 1) {
+        const bool up = nl & bit;
+#pragma unroll
+        for (int i = 0; i < M / 2; ++i)
+          if (i < m / 2) {
+            const float keep = up ? v[i + m / 2] : v[i], send = up ? v[i] : v[i + m / 2];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, bit * STEP);
+          }
+        m /= 2;
+      } else {
+        v[0] += __shfl_xor_sync(0xffffffffu, v[0], bit * STEP);
+      }
+    }
+  }
+  // index of the first value that lane nl ends with
+  __device__ static __forceinline__ int first(int nl) {
+    int f = 0, m = M;
+#pragma unroll
+    for (int bit = 1; bit < NL; bit *= 2)
+      if (m > 1) {
+        m /= 2;
+        if (nl & bit) f += m;
+      }
+    return f;
+  }
+};
+
+// M consecutive floats of shared memory as one load
+template <int M>
+__device__ __forceinline__ void lds(float (&v)[M], const float *p) {
+  const Vec<float, M> q = *reinterpret_cast<const Vec<float, M> *>(p);
+#pragma unroll
+  for (int i = 0; i < M; ++i) v[i] = q.e[i];
+}
+
+// Lanes that share a channel for N states.
+inline int lanes_of(int N) {
+  int nl = 2;
+  while (nl * SPL < N) nl *= 2;
+  return nl;
+}
+
+// Heads that share B and C and lie next to one another in every token row are
+// one wider head (parameters and states are [H, d, ..] blocks, so they follow).
+inline void collapse(Scan &c, std::initializer_list<Str *> ss) {
+  const int each = c.H / c.G;
+  if (each == 1) return;
+  for (Str *s : ss)
+    if (s->h != c.d) return;
+  c.d *= each;
+  c.H = c.G;
+  for (Str *s : ss) s->h *= each;
+}
+
+}  // namespace mix
+}  // namespace tmem

@@ -1,0 +1,597 @@
+// Gradients of the selective scan. With k_t = dy_t silu(z_t) and g_t = dL/dh_t:
+//   g_t = Cm_t k_t + a_{t+1} g_{t+1},   a_t = exp(e_t A)
+//   d(e x)_t = sum_n g_t Bm_t,          dx_t = e_t d(e x)_t + D k_t
+//   de_t = x_t d(e x)_t + sum_n A g_t a_t h_{t-1},  ddt_t = de_t softplus'(dt_t + bias)
+//   dA = sum_{b,t} e_t g_t a_t h_{t-1},  dB_t = sum_c g_t e_t x_t,  dC_t = sum_c k_t h_t
+//   dz_t = dy_t silu'(z_t) (sum_n Cm_t h_t + D x_t),  dD = sum_{b,t} k_t x_t
+//
+// Two passes over the tokens. The first walks forward and keeps the state at
+// every 8th token (fp32). The second walks the 8-token tiles backward: from a
+// kept state it forms the tile's 8 decays and states again, holds both in
+// registers (2 channels x 4 states x 8 tokens a lane), and takes the tile's
+// tokens in reverse. exp() is so evaluated twice per (token, channel, state)
+// in all, and no state is read back from memory but the kept ones.
+// When there are few channels the sequence is split into segments that both
+// passes take at the same time: the first pass starts each from a zero state
+// and also forms what the segment adds to the gradient that enters it from
+// behind, sum_t (prod a up to t) Cm_t k_t; the second joins the segments before
+// (state) and after (gradient) its own, with the segments' decays exp(A sum e).
+#include "tm_scan.cuh"
+
+namespace tmem {
+namespace mix {
+namespace {
+
+using bf16 = __nv_bfloat16;
+constexpr int K = 8;                 // tokens between kept states
+constexpr int CPL = 2;               // channels of a lane
+constexpr int TF = 16;               // tokens of the first pass's tile
+constexpr int MAXW = 4;              // warps of a CTA
+
+struct Plan {
+  int warps, blocks, S, L;           // as in the forward
+  int NP;                            // padded states
+  size_t ck, cume, hloc, gloc, esum, bc, pa, pd, total;   // offsets into the workspace, in floats
+  int pbn;                           // partials of dB and dC: (head of the group, channel block)
+};
+
+Plan plan_of(int B, int H, int G, int T, int d, int N) {
+  const int NL = lanes_of(N), CW = 32 / NL * CPL;
+  Plan p;
+  p.NP = NL * SPL;
+  p.warps = MAXW;
+  while (p.warps > 1 && CW * p.warps / 2 >= d) p.warps /= 2;
+  p.blocks = (d + CW * p.warps - 1) / (CW * p.warps);
+  // two CTAs of 4 warps fit on an SM; a split costs the first pass the
+  // gradient sums and the joins, so it has to at least double the CTAs
+  const long long ctas = (long long)B * H * p.blocks * p.warps / MAXW + 1;
+  long long S = 2LL * kSMs / ctas;
+  const long long most = T / 64;
+  if (S > most) S = most;
+  if (S < 2) S = 1;
+  p.L = (int)(((T + S - 1) / S + TF - 1) / TF * TF);
+  p.S = (T + p.L - 1) / p.L;
+  const size_t chans = (size_t)B * H * d, tiles = ((size_t)T + K - 1) / K;
+  p.pbn = H / G * p.blocks;
+  size_t off = 0;
+  auto take = [&](size_t n) {
+    const size_t at = off;
+    off += (n + 63) / 64 * 64;
+    return at;
+  };
+  p.ck = take(tiles * chans * p.NP);
+  p.cume = take(p.S > 1 ? tiles * chans : 0);
+  p.hloc = take(p.S > 1 ? p.S * chans * p.NP : 0);
+  p.gloc = take(p.S > 1 ? p.S * chans * p.NP : 0);
+  p.esum = take(p.S > 1 ? p.S * chans : 0);
+  p.bc = take((size_t)p.pbn * B * G * T * 2 * p.NP);
+  p.pa = take((size_t)B * p.S * H * d * p.NP);
+  p.pd = take((size_t)B * p.S * 2 * H * d);
+  p.total = off;
+  return p;
+}
+
+struct Where {
+  int seg, cb, h, b, g;
+};
+__device__ __forceinline__ Where where(const Scan &a, const Plan &pl) {
+  Where w;
+  unsigned blk = blockIdx.x;
+  w.seg = blk % pl.S;
+  blk /= pl.S;
+  w.cb = blk % pl.blocks;
+  blk /= pl.blocks;
+  w.h = blk % a.H;
+  w.b = blk / a.H;
+  w.g = w.h / (a.H / a.G);
+  return w;
+}
+
+// First pass: states at every K-th token.
+template <typename T, int NL, int V, bool SPLIT>
+__global__ void __launch_bounds__(32 * MAXW) states_kernel(const Scan a, const Plan pl, float *ws) {
+  constexpr int NP = NL * SPL, CW = 32 / NL * CPL;
+  constexpr int TILE = TF * CW / V;                     // vectors of a warp's share of a tile
+  constexpr int NV = TILE >= 32 ? TILE / 32 : 1;
+  extern __shared__ __align__(16) float sm[];
+  const int CB = CW * pl.warps;
+  float *s_e = sm, *s_u = s_e + TF * CB, *s_k = s_u + TF * CB, *s_B = s_k + (SPLIT ? TF * CB : 0), *s_C = s_B + TF * NP;
+  const Where w = where(a, pl);
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, nl = lane % NL, cl = lane / NL;
+  const int nthr = 32 * pl.warps, n0 = nl * SPL, N = a.N;
+  const int c_blk = w.cb * CB, c0 = warp * CW + cl * CPL;
+  const long long bh = (long long)w.b * a.H + w.h;
+  const int n_tok = tokens_of(a.lengths, w.b, a.T);
+  const long long t_seg = (long long)w.seg * pl.L;
+  const long long t_end = t_seg + pl.L < n_tok ? t_seg + pl.L : n_tok;
+  const long long per = (long long)a.B * a.H * a.d, chan = bh * a.d + c_blk + c0;
+  float *ck = ws + pl.ck, *cume = ws + pl.cume;
+
+  float A2[CPL][SPL], hs[CPL][SPL], P[CPL][SPL], Gs[CPL][SPL], es[CPL];
+#pragma unroll
+  for (int c = 0; c < CPL; ++c) {
+    es[c] = 0.f;
+#pragma unroll
+    for (int s = 0; s < SPL; ++s) {
+      const bool live = c_blk + c0 + c < a.d && n0 + s < N;
+      A2[c][s] = live ? a.A[((long long)w.h * a.d + c_blk + c0 + c) * N + n0 + s] * kLog2e : 0.f;
+      hs[c][s] = live && a.state0 && w.seg == 0 ? a.state0[(chan + c) * N + n0 + s] : 0.f;
+      P[c][s] = 1.f;
+      Gs[c][s] = 0.f;
+    }
+  }
+  const int vpr = CB / V, vlog = __ffs(vpr) - 1, vtile = TF * vpr;
+  const T *xp = static_cast<const T *>(a.x) + w.b * a.sx.b + w.h * a.sx.h + c_blk;
+  const T *dp = static_cast<const T *>(a.dt) + w.b * a.sdt.b + w.h * a.sdt.h + c_blk;
+  const T *zp = a.z ? static_cast<const T *>(a.z) + w.b * a.sz.b + w.h * a.sz.h + c_blk : nullptr;
+  const T *yp = static_cast<const T *>(a.dy) + w.b * a.sdy.b + w.h * a.sdy.h + c_blk;
+  const T *Bp = static_cast<const T *>(a.Bm) + w.b * a.sB.b + w.g * a.sB.h;
+  const T *Cp = static_cast<const T *>(a.Cm) + w.b * a.sC.b + w.g * a.sC.h;
+
+  Vec<T, V> xr[NV], dr[NV], zr[NV], yr[NV];
+  auto fetch = [&](long long t0) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int i = tid + k * nthr, c = (i & (vpr - 1)) * V;
+      const long long t = t0 + (i >> vlog);
+      const bool live = i < vtile && c_blk + c < a.d && t < t_end;
+      xr[k] = load_if<T, V>(xp + t * a.sx.t + c, live);
+      dr[k] = load_if<T, V>(dp + t * a.sdt.t + c, live);
+      if (SPLIT) {
+        zr[k] = load_if<T, V>(zp + t * a.sz.t + c, live && zp);
+        yr[k] = load_if<T, V>(yp + t * a.sdy.t + c, live);
+      }
+    }
+  };
+  fetch(t_seg);
+  for (long long t0 = t_seg; t0 < t_end; t0 += TF) {
+    for (int i = tid; i < TF * NP; i += nthr) {
+      const int t = i / NP, n = i % NP;
+      const bool live = t0 + t < t_end && n < N;
+      s_B[i] = live ? to_f(Bp[(t0 + t) * a.sB.t + n]) : 0.f;
+      if (SPLIT) s_C[i] = live ? to_f(Cp[(t0 + t) * a.sC.t + n]) : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int i = tid + k * nthr, kc = (i & (vpr - 1)) * V, t = i >> vlog;
+      if (i >= vtile) continue;
+      const bool live = c_blk + kc < a.d && t0 + t < t_end;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        float e = get(dr[k], j) + (live && a.dt_bias ? a.dt_bias[(long long)w.h * a.d + c_blk + kc + j] : 0.f);
+        if (a.softplus) e = softplus(e);
+        e = live ? e : 0.f;
+        s_e[t * CB + kc + j] = e;
+        s_u[t * CB + kc + j] = e * get(xr[k], j);
+        if (SPLIT) s_k[t * CB + kc + j] = get(yr[k], j) * (zp ? silu(get(zr[k], j)) : 1.f);
+      }
+    }
+    __syncthreads();
+    fetch(t0 + TF);
+#pragma unroll
+    for (int t = 0; t < TF; ++t) {
+      if (t % K == 0 && t0 + t < t_end) {
+        const long long tile = (t0 + t) / K;
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) {
+          if (c_blk + c0 + c >= a.d) continue;
+          const long long at = tile * per + chan + c;
+          *reinterpret_cast<float4 *>(ck + at * NP + n0) = make_float4(hs[c][0], hs[c][1], hs[c][2], hs[c][3]);
+          if (SPLIT && nl == 0) cume[at] = es[c];
+        }
+      }
+      float e[CPL], u[CPL], k[CPL], B[SPL], C[SPL];
+      lds<CPL>(e, s_e + t * CB + c0);
+      lds<CPL>(u, s_u + t * CB + c0);
+      lds<SPL>(B, s_B + t * NP + n0);
+      if (SPLIT) {
+        lds<CPL>(k, s_k + t * CB + c0);
+        lds<SPL>(C, s_C + t * NP + n0);
+      }
+#pragma unroll
+      for (int c = 0; c < CPL; ++c) {
+        if (SPLIT) es[c] += e[c];
+#pragma unroll
+        for (int s = 0; s < SPL; ++s) {
+          const float av = ex2(e[c] * A2[c][s]);
+          hs[c][s] = fmaf(av, hs[c][s], u[c] * B[s]);
+          if (SPLIT) {
+            P[c][s] *= av;
+            Gs[c][s] = fmaf(P[c][s], C[s] * k[c], Gs[c][s]);
+          }
+        }
+      }
+    }
+    __syncthreads();
+  }
+  if (SPLIT)
+#pragma unroll
+    for (int c = 0; c < CPL; ++c) {
+      if (c_blk + c0 + c >= a.d) continue;
+      const long long at = w.seg * per + chan + c;
+      if (nl == 0) ws[pl.esum + at] = es[c];
+      *reinterpret_cast<float4 *>(ws + pl.hloc + at * NP + n0) = make_float4(hs[c][0], hs[c][1], hs[c][2], hs[c][3]);
+      *reinterpret_cast<float4 *>(ws + pl.gloc + at * NP + n0) = make_float4(Gs[c][0], Gs[c][1], Gs[c][2], Gs[c][3]);
+    }
+}
+
+// Second pass: the gradients.
+template <typename T, int NL, int V, bool SPLIT>
+__global__ void __launch_bounds__(32 * MAXW, 2) grad_kernel(const Scan a, const Plan pl, float *ws) {
+  constexpr int NP = NL * SPL, CW = 32 / NL * CPL;
+  constexpr int TILE = K * CW / V;
+  constexpr int NV = TILE >= 32 ? TILE / 32 : 1;
+  using SumN = LaneSum<2 * CPL, NL>;                    // d(e x) and A-part of de of the lane's channels
+  using SumY = LaneSum<CPL, NL>;
+  using SumC = LaneSum<2 * SPL, 32 / NL, NL>;           // dB and dC of the lane's states
+  extern __shared__ __align__(16) float sm[];
+  const int CB = CW * pl.warps;
+  float *s_e = sm, *s_u = s_e + K * CB, *s_k = s_u + K * CB, *s_B = s_k + K * CB, *s_C = s_B + K * NP,
+        *s_bc = s_C + K * NP;                           // [warps][K][2 NP]
+  const Where w = where(a, pl);
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, nl = lane % NL, cl = lane / NL;
+  const int nthr = 32 * pl.warps, n0 = nl * SPL, N = a.N;
+  const int c_blk = w.cb * CB, c0 = warp * CW + cl * CPL;
+  const long long bh = (long long)w.b * a.H + w.h;
+  const int n_tok = tokens_of(a.lengths, w.b, a.T);
+  const long long t_seg = (long long)w.seg * pl.L;
+  const long long t_all = t_seg + pl.L < a.T ? t_seg + pl.L : a.T;
+  const long long per = (long long)a.B * a.H * a.d, chan = bh * a.d + c_blk + c0;
+  const float *ck = ws + pl.ck, *cume = ws + pl.cume;
+
+  float A2[CPL][SPL], R[CPL][SPL], dA[CPL][SPL], hin[CPL][SPL];
+#pragma unroll
+  for (int c = 0; c < CPL; ++c)
+#pragma unroll
+    for (int s = 0; s < SPL; ++s) {
+      const bool live = c_blk + c0 + c < a.d && n0 + s < N;
+      A2[c][s] = live ? a.A[((long long)w.h * a.d + c_blk + c0 + c) * N + n0 + s] * kLog2e : 0.f;
+      R[c][s] = live && a.dstate_end ? a.dstate_end[(chan + c) * N + n0 + s] : 0.f;
+      dA[c][s] = hin[c][s] = 0.f;
+    }
+  if (SPLIT)
+#pragma unroll
+    for (int c = 0; c < CPL; ++c) {
+      if (c_blk + c0 + c >= a.d) continue;
+      for (int q = 0; q < w.seg; ++q) {
+        const long long at = q * per + chan + c;
+        const float es = ws[pl.esum + at];
+        float l[SPL];
+        lds<SPL>(l, ws + pl.hloc + at * NP + n0);
+#pragma unroll
+        for (int s = 0; s < SPL; ++s) hin[c][s] = q == 0 ? l[s] : fmaf(ex2(A2[c][s] * es), hin[c][s], l[s]);
+      }
+      for (int q = pl.S - 1; q > w.seg; --q) {
+        const long long at = q * per + chan + c;
+        const float es = ws[pl.esum + at];
+        float l[SPL];
+        lds<SPL>(l, ws + pl.gloc + at * NP + n0);
+#pragma unroll
+        for (int s = 0; s < SPL; ++s) R[c][s] = fmaf(ex2(A2[c][s] * es), R[c][s], l[s]);
+      }
+    }
+
+  const int vpr = CB / V, vlog = __ffs(vpr) - 1, vtile = K * vpr;
+  const long long hd = (long long)w.h * a.d + c_blk;
+  const T *xp = static_cast<const T *>(a.x) + w.b * a.sx.b + w.h * a.sx.h + c_blk;
+  const T *dp = static_cast<const T *>(a.dt) + w.b * a.sdt.b + w.h * a.sdt.h + c_blk;
+  const T *zp = a.z ? static_cast<const T *>(a.z) + w.b * a.sz.b + w.h * a.sz.h + c_blk : nullptr;
+  const T *yp = static_cast<const T *>(a.dy) + w.b * a.sdy.b + w.h * a.sdy.h + c_blk;
+  const T *Bp = static_cast<const T *>(a.Bm) + w.b * a.sB.b + w.g * a.sB.h;
+  const T *Cp = static_cast<const T *>(a.Cm) + w.b * a.sC.b + w.g * a.sC.h;
+  T *dxp = static_cast<T *>(a.dx) + w.b * a.sdx.b + w.h * a.sdx.h + c_blk;
+  T *ddp = static_cast<T *>(a.ddt) + w.b * a.sddt.b + w.h * a.sddt.h + c_blk;
+  T *dzp = a.dz ? static_cast<T *>(a.dz) + w.b * a.sdz.b + w.h * a.sdz.h + c_blk : nullptr;
+  float *bc = ws + pl.bc + ((((long long)(w.h % (a.H / a.G)) * pl.blocks + w.cb) * a.B + w.b) * a.G + w.g) * a.T * 2 * NP;
+
+  float sumD[NV][V], sumb[NV][V];
+#pragma unroll
+  for (int k = 0; k < NV; ++k)
+#pragma unroll
+    for (int j = 0; j < V; ++j) sumD[k][j] = sumb[k][j] = 0.f;
+
+  const long long tiles = (t_all - t_seg + K - 1) / K;
+  for (long long tl = tiles - 1; tl >= 0; --tl) {
+    const long long t0 = t_seg + tl * K;
+    if (t0 >= n_tok) {                                  // behind the sequence's end: zero gradients
+      for (int k = 0; k < NV; ++k) {
+        const int i = tid + k * nthr, kc = (i & (vpr - 1)) * V, t = i >> vlog;
+        if (i >= vtile || c_blk + kc >= a.d || t0 + t >= t_all) continue;
+        Vec<T, V> o;
+#pragma unroll
+        for (int j = 0; j < V; ++j) put(o, j, 0.f);
+        store(dxp + (t0 + t) * a.sdx.t + kc, o);
+        store(ddp + (t0 + t) * a.sddt.t + kc, o);
+        if (dzp) store(dzp + (t0 + t) * a.sdz.t + kc, o);
+      }
+      for (int i = tid; i < K * 2 * NP; i += nthr)
+        if (t0 + i / (2 * NP) < t_all) bc[t0 * 2 * NP + i] = 0.f;
+      continue;
+    }
+    // stage the tile
+    Vec<T, V> xk[NV], dk[NV], zk[NV], yk[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int i = tid + k * nthr, kc = (i & (vpr - 1)) * V, t = i >> vlog;
+      const bool live = i < vtile && c_blk + kc < a.d && t0 + t < n_tok;
+      xk[k] = load_if<T, V>(xp + (t0 + t) * a.sx.t + kc, live);
+      dk[k] = load_if<T, V>(dp + (t0 + t) * a.sdt.t + kc, live);
+      zk[k] = load_if<T, V>(zp + (t0 + t) * a.sz.t + kc, live && zp);
+      yk[k] = load_if<T, V>(yp + (t0 + t) * a.sdy.t + kc, live);
+    }
+    float h0[CPL][SPL];
+#pragma unroll
+    for (int c = 0; c < CPL; ++c) {
+      const long long at = t0 / K * per + chan + c;
+      const bool in = c_blk + c0 + c < a.d;
+      const Vec<float, SPL> q = load_if<float, SPL>(ck + at * NP + n0, in);
+      const float es = SPLIT && w.seg > 0 && in ? cume[at] : 0.f;
+#pragma unroll
+      for (int s = 0; s < SPL; ++s) h0[c][s] = SPLIT && w.seg > 0 ? fmaf(ex2(A2[c][s] * es), hin[c][s], q.e[s]) : q.e[s];
+    }
+    for (int i = tid; i < K * NP; i += nthr) {
+      const int t = i / NP, n = i % NP;
+      const bool live = t0 + t < n_tok && n < N;
+      s_B[i] = live ? to_f(Bp[(t0 + t) * a.sB.t + n]) : 0.f;
+      s_C[i] = live ? to_f(Cp[(t0 + t) * a.sC.t + n]) : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int i = tid + k * nthr, kc = (i & (vpr - 1)) * V, t = i >> vlog;
+      if (i >= vtile) continue;
+      const bool live = c_blk + kc < a.d && t0 + t < n_tok;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        float e = get(dk[k], j) + (live && a.dt_bias ? a.dt_bias[hd + kc + j] : 0.f);
+        if (a.softplus) e = softplus(e);
+        e = live ? e : 0.f;
+        s_e[t * CB + kc + j] = e;
+        s_u[t * CB + kc + j] = e * get(xk[k], j);
+        s_k[t * CB + kc + j] = get(yk[k], j) * (zp ? silu(get(zk[k], j)) : 1.f);
+      }
+    }
+    __syncthreads();
+
+    // the tile's decays and states again
+    float av[K][CPL][SPL], hv[K][CPL][SPL];
+#pragma unroll
+    for (int t = 0; t < K; ++t) {
+      float e[CPL], u[CPL], B[SPL];
+      lds<CPL>(e, s_e + t * CB + c0);
+      lds<CPL>(u, s_u + t * CB + c0);
+      lds<SPL>(B, s_B + t * NP + n0);
+#pragma unroll
+      for (int c = 0; c < CPL; ++c)
+#pragma unroll
+        for (int s = 0; s < SPL; ++s) {
+          av[t][c][s] = ex2(e[c] * A2[c][s]);
+          hv[t][c][s] = fmaf(av[t][c][s], t ? hv[t ? t - 1 : 0][c][s] : h0[c][s], u[c] * B[s]);
+        }
+    }
+#pragma unroll
+    for (int t = K - 1; t >= 0; --t) {
+      float e[CPL], u[CPL], kk[CPL], B[SPL], C[SPL];
+      lds<CPL>(e, s_e + t * CB + c0);
+      lds<CPL>(u, s_u + t * CB + c0);
+      lds<CPL>(kk, s_k + t * CB + c0);
+      lds<SPL>(B, s_B + t * NP + n0);
+      lds<SPL>(C, s_C + t * NP + n0);
+      float un[2 * CPL], y[CPL], bcv[2 * SPL];
+#pragma unroll
+      for (int i = 0; i < 2 * CPL; ++i) un[i] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 2 * SPL; ++i) bcv[i] = 0.f;
+#pragma unroll
+      for (int c = 0; c < CPL; ++c) {
+        y[c] = 0.f;
+#pragma unroll
+        for (int s = 0; s < SPL; ++s) {
+          const float h = hv[t][c][s], hp = t ? hv[t ? t - 1 : 0][c][s] : h0[c][s];
+          const float g = fmaf(C[s], kk[c], R[c][s]);
+          y[c] = fmaf(C[s], h, y[c]);
+          bcv[SPL + s] = fmaf(kk[c], h, bcv[SPL + s]);
+          bcv[s] = fmaf(g, u[c], bcv[s]);
+          un[c] = fmaf(g, B[s], un[c]);
+          R[c][s] = g * av[t][c][s];
+          const float q = R[c][s] * hp;
+          dA[c][s] = fmaf(q, e[c], dA[c][s]);
+          un[CPL + c] = fmaf(q, A2[c][s], un[CPL + c]);
+        }
+      }
+      SumN::run(un, nl);
+      if (zp) SumY::run(y, nl);
+      SumC::run(bcv, cl);
+      // every lane of the channel has read e, u and k of this token
+      if (nl < SumN::writers) {
+        const int f = SumN::first(nl);
+#pragma unroll
+        for (int i = 0; i < SumN::kept; ++i) {
+          const int at = f + i;
+          if (at < CPL) s_u[t * CB + c0 + at] = un[i];
+          else s_e[t * CB + c0 + at - CPL] = un[i];
+        }
+      }
+      if (zp && nl < SumY::writers) {
+        const int f = SumY::first(nl);
+#pragma unroll
+        for (int i = 0; i < SumY::kept; ++i) s_k[t * CB + c0 + f + i] = y[i];
+      }
+      if (cl < SumC::writers) {
+        const int f = SumC::first(cl);
+#pragma unroll
+        for (int i = 0; i < SumC::kept; ++i) {
+          const int at = f + i;
+          s_bc[(warp * K + t) * 2 * NP + (at < SPL ? n0 + at : NP + n0 + at - SPL)] = bcv[i];
+        }
+      }
+    }
+    __syncthreads();
+    // the thread that staged an element finishes its gradients
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int i = tid + k * nthr, kc = (i & (vpr - 1)) * V, t = i >> vlog;
+      if (i >= vtile || c_blk + kc >= a.d || t0 + t >= t_all) continue;
+      const bool live = t0 + t < n_tok;
+      Vec<T, V> ox, od, oz;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const float v = get(dk[k], j) + (a.dt_bias ? a.dt_bias[hd + kc + j] : 0.f);
+        const float D = a.D ? a.D[hd + kc + j] : 0.f;
+        const float x = get(xk[k], j), dy = get(yk[k], j), z = get(zk[k], j);
+        const float e = a.softplus ? softplus(v) : v;
+        const float q = zp ? sigmoid(z) : 0.f;
+        const float kk = zp ? dy * z * q : dy;
+        const float du = s_u[t * CB + kc + j], de = s_e[t * CB + kc + j] * (1.f / kLog2e);
+        float dd = fmaf(du, x, de);
+        if (a.softplus) dd *= sigmoid(v);
+        dd = live ? dd : 0.f;
+        put(ox, j, live ? fmaf(du, e, D * kk) : 0.f);
+        put(od, j, dd);
+        if (zp) put(oz, j, live ? dy * (q * fmaf(z, 1.f - q, 1.f)) * fmaf(D, x, s_k[t * CB + kc + j]) : 0.f);
+        sumD[k][j] = fmaf(kk, x, sumD[k][j]);
+        sumb[k][j] += dd;
+      }
+      store(dxp + (t0 + t) * a.sdx.t + kc, ox);
+      store(ddp + (t0 + t) * a.sddt.t + kc, od);
+      if (dzp) store(dzp + (t0 + t) * a.sdz.t + kc, oz);
+    }
+    for (int i = tid; i < K * 2 * NP; i += nthr) {
+      float s = 0.f;
+      for (int q = 0; q < pl.warps; ++q) s += s_bc[q * K * 2 * NP + i];
+      if (t0 + i / (2 * NP) < t_all) bc[t0 * 2 * NP + i] = s;
+    }
+  }
+
+  // the segment's part of dA, dD and d(dt_bias)
+  const long long HD = (long long)a.H * a.d, part = (long long)w.b * pl.S + w.seg;
+#pragma unroll
+  for (int c = 0; c < CPL; ++c) {
+    if (c_blk + c0 + c >= a.d) continue;
+    *reinterpret_cast<float4 *>(ws + pl.pa + (part * HD + hd + c0 + c) * NP + n0) =
+        make_float4(dA[c][0], dA[c][1], dA[c][2], dA[c][3]);
+    if (w.seg == 0 && a.dstate0)
+#pragma unroll
+      for (int s = 0; s < SPL; ++s)
+        if (n0 + s < N) a.dstate0[(chan + c) * N + n0 + s] = R[c][s];
+  }
+  for (int p = 0; p < 2; ++p) {
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int i = tid + k * nthr, kc = (i & (vpr - 1)) * V, t = i >> vlog;
+      if (i >= vtile) continue;
+#pragma unroll
+      for (int j = 0; j < V; ++j) s_e[t * CB + kc + j] = p ? sumb[k][j] : sumD[k][j];
+    }
+    __syncthreads();
+    for (int c = tid; c < CB; c += nthr) {
+      if (c_blk + c >= a.d) continue;
+      float s = 0.f;
+#pragma unroll
+      for (int t = 0; t < K; ++t) s += s_e[t * CB + c];
+      ws[pl.pd + (part * 2 + p) * HD + hd + c] = s;
+    }
+  }
+}
+
+// dB and dC: the partials of the channel blocks that share them, in order.
+template <typename T>
+__global__ void __launch_bounds__(256) join_bc_kernel(const Scan a, const Plan pl, const float *bc) {
+  const long long rows = (long long)a.B * a.G * a.T, i = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (i >= rows * 2 * pl.NP) return;
+  const long long row = i / (2 * pl.NP);
+  const int q = (int)(i % (2 * pl.NP)), n = q % pl.NP;
+  if (n >= a.N) return;
+  float s = 0.f;
+  for (int p = 0; p < pl.pbn; ++p) s += bc[p * rows * 2 * pl.NP + i];
+  Vec<T, 1> o;
+  put(o, 0, s);
+  static_cast<T *>(q < pl.NP ? a.dB : a.dC)[row * a.N + n] = o.e[0];
+}
+
+// dA, dD and d(dt_bias): the partials of the sequences and segments, in order.
+__global__ void __launch_bounds__(256) join_param_kernel(const Scan a, const Plan pl, const float *ws) {
+  __shared__ float red[8][32];
+  const long long HD = (long long)a.H * a.d, nA = HD * pl.NP, n = nA + 2 * HD;
+  const long long i = (long long)blockIdx.x * 32 + threadIdx.x % 32;
+  const int k = threadIdx.x / 32, parts = a.B * pl.S;
+  float s = 0.f;
+  if (i < n)
+    for (int p = k; p < parts; p += 8) s += i < nA ? ws[pl.pa + p * nA + i] : ws[pl.pd + p * 2 * HD + (i - nA)];
+  red[k][threadIdx.x % 32] = s;
+  __syncthreads();
+  if (k || i >= n) return;
+  s = 0.f;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) s += red[q][threadIdx.x];
+  if (i < nA) {
+    const int st = (int)(i % pl.NP);
+    if (st < a.N) a.dA[i / pl.NP * a.N + st] = s;
+  } else if (i < nA + HD) {
+    if (a.dD) a.dD[i - nA] = s;
+  } else if (a.ddt_bias) {
+    a.ddt_bias[i - nA - HD] = s;
+  }
+}
+
+template <typename T, int NL, int VF, int VB>
+cudaError_t run(const Scan &c, cudaStream_t st) {
+  constexpr int NP = NL * SPL, CW = 32 / NL * CPL;
+  const Plan p = plan_of(c.B, c.H, c.G, c.T, c.d, c.N);
+  const int CB = CW * p.warps;
+  float *ws = static_cast<float *>(c.ws);
+  const long long grid = (long long)c.B * c.H * p.blocks * p.S;
+  const long long nbc = (long long)c.B * c.G * c.T * 2 * NP;
+  if (grid > 0x7fffffffLL || (nbc + 255) / 256 > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const int thr = 32 * p.warps;
+  const bool split = p.S > 1;
+  const size_t sm1 = ((split ? 3 : 2) * TF * CB + 2 * TF * NP) * 4;
+  const size_t sm2 = (3 * K * CB + 2 * K * NP + p.warps * K * 2 * NP) * 4;
+  if (split) states_kernel<T, NL, VF, true><<<(unsigned)grid, thr, sm1, st>>>(c, p, ws);
+  else states_kernel<T, NL, VF, false><<<(unsigned)grid, thr, sm1, st>>>(c, p, ws);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  if (split) grad_kernel<T, NL, VB, true><<<(unsigned)grid, thr, sm2, st>>>(c, p, ws);
+  else grad_kernel<T, NL, VB, false><<<(unsigned)grid, thr, sm2, st>>>(c, p, ws);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  join_bc_kernel<T><<<(unsigned)((nbc + 255) / 256), 256, 0, st>>>(c, p, ws + p.bc);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const long long n = (long long)c.H * c.d * (NP + 2);
+  join_param_kernel<<<(unsigned)((n + 31) / 32), 256, 0, st>>>(c, p, ws);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t dispatch(const Scan &c, cudaStream_t st) {
+  const int el = sizeof(T);
+  auto vec = [&](int V) {
+    return fits(c.x, c.sx, c.d, V, el) && fits(c.dt, c.sdt, c.d, V, el) && fits(c.z, c.sz, c.d, V, el) &&
+           fits(c.dy, c.sdy, c.d, V, el) && fits(c.dx, c.sdx, c.d, V, el) && fits(c.ddt, c.sddt, c.d, V, el) &&
+           fits(c.dz, c.sdz, c.d, V, el);
+  };
+  switch (lanes_of(c.N)) {
+    case 2: return vec(4) ? run<T, 2, 4, 4>(c, st) : run<T, 2, 1, 1>(c, st);
+    case 4: return vec(4) ? run<T, 4, 4, 4>(c, st) : run<T, 4, 1, 1>(c, st);
+    case 8: return vec(2) ? run<T, 8, 2, 2>(c, st) : run<T, 8, 1, 1>(c, st);
+    case 16: return vec(2) ? run<T, 16, 2, 1>(c, st) : run<T, 16, 1, 1>(c, st);
+    default: return run<T, 32, 1, 1>(c, st);
+  }
+}
+
+}  // namespace
+
+size_t scan_backward_ws(int B, int H, int G, int T, int d, int N) {
+  const size_t one = plan_of(B, H, G, T, d, N).total, joined = plan_of(B, G, G, T, H / G * d, N).total;
+  return up256((one > joined ? one : joined) * 4);
+}
+
+cudaError_t scan_backward_launch(Scan c, cudaStream_t st) {
+  if (c.z) collapse(c, {&c.sx, &c.sdt, &c.sz, &c.sdy, &c.sdx, &c.sddt, &c.sdz});
+  else collapse(c, {&c.sx, &c.sdt, &c.sdy, &c.sdx, &c.sddt});
+  return c.bf16 ? dispatch<bf16>(c, st) : dispatch<float>(c, st);
+}
+
+}  // namespace mix
+}  // namespace tmem
