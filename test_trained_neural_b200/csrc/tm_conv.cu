@@ -41,8 +41,49 @@ __device__ __forceinline__ Vec<T, V> row_of(const T *x, long long st, const T *h
   return load_if<T, V>(hist + (w - 1 + t) * d, live && hist != nullptr && w - 1 + t >= 0);
 }
 
+// V floats at p, `live` or zeros; one 16-byte load where V is 4.
+template <int V>
+__device__ __forceinline__ void floats(float (&v)[V], const float *p, bool live) {
+  if (V == 4 && reinterpret_cast<uintptr_t>(p) % 16 == 0) {
+    const Vec<float, V> q = load_if<float, V>(p, live);
+#pragma unroll
+    for (int e = 0; e < V; ++e) v[e] = q.e[e];
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; ++e) v[e] = live ? p[e] : 0.f;
+  }
+}
+// The filter taps and the bias of V channels, taps beyond the filter zero.
+template <int V, int MAXW>
+__device__ __forceinline__ void taps_of(float (&f)[MAXW][V], float (&bias)[V], const Conv &a, long long ch, bool live) {
+  const float *fp = a.filt + ch * a.w;
+  if (MAXW == 4 && a.w == 4) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      float q[4];
+      floats<4>(q, fp + 4 * e, live);
+#pragma unroll
+      for (int j = 0; j < MAXW; ++j) f[j][e] = q[j & 3];
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+#pragma unroll
+      for (int j = 0; j < MAXW; ++j) f[j][e] = live && j < a.w ? fp[e * a.w + j] : 0.f;
+  }
+  if (a.bias) {
+    floats<V>(bias, a.bias + ch, live);
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; ++e) bias[e] = 0.f;
+  }
+}
+
+// A thread walks `run` rows in batches of RB, the next batch's loads issued
+// before the current one is computed; the w - 1 rows before a batch stay in
+// registers, and the taps are read once for the whole run.
 template <typename T, int V, int MAXW, int RB>
-__global__ void __launch_bounds__(NT) conv_kernel(const Conv a, const Split sp) {
+__global__ void __launch_bounds__(NT, MAXW <= 4 ? 3 : 2) conv_kernel(const Conv a, const Split sp, const int run) {
   unsigned blk = blockIdx.x;
   const int tile = blk % sp.tiles;
   blk /= sp.tiles;
@@ -55,7 +96,8 @@ __global__ void __launch_bounds__(NT) conv_kernel(const Conv a, const Split sp) 
   const int n = tokens_of(a.lengths, b, a.T);
   const T *x = static_cast<const T *>(a.x) + b * a.sx.b + h * a.sx.h + c;
   const T *hist = a.hist ? static_cast<const T *>(a.hist) + ((long long)b * a.H + h) * (w - 1) * d + c : nullptr;
-  const long long t0 = ((long long)tile * sp.RL + rl) * RB;
+  const long long t0 = ((long long)tile * sp.RL + rl) * run;
+  const long long t1 = t0 + run < n ? t0 + run : n;
 
   // the tail: rows n - (w - 1) .. n - 1 of history and tokens
   if (a.tail && tile == 0) {
@@ -65,33 +107,38 @@ __global__ void __launch_bounds__(NT) conv_kernel(const Conv a, const Split sp) 
   }
   if (t0 >= n) return;
 
-  Vec<T, V> raw[RB + MAXW - 1];
+  Vec<T, V> raw[RB + MAXW - 1], next[RB];
 #pragma unroll
-  for (int i = 0; i < RB + MAXW - 1; ++i) {
-    const long long t = t0 - (MAXW - 1) + i;
-    raw[i] = row_of<T, V>(x, a.sx.t, hist, w, d, t, i + w >= MAXW && t < n);
-  }
-  const float *fp = a.filt + ((long long)h * d + c) * w;
+  for (int i = 0; i < MAXW - 1; ++i)
+    raw[i] = row_of<T, V>(x, a.sx.t, hist, w, d, t0 - (MAXW - 1) + i, i + w >= MAXW);
+  const T *xp = x + t0 * a.sx.t;
+#pragma unroll
+  for (int i = 0; i < RB; ++i) next[i] = load_if<T, V>(xp + i * a.sx.t, t0 + i < t1);
   float f[MAXW][V], bias[V];
+  taps_of<V, MAXW>(f, bias, a, (long long)h * d + c, true);
+  T *y = static_cast<T *>(a.y) + b * a.sy.b + h * a.sy.h + c + t0 * a.sy.t;
+  for (long long tb = t0; tb < t1; tb += RB) {
 #pragma unroll
-  for (int e = 0; e < V; ++e) {
-    bias[e] = a.bias ? a.bias[(long long)h * d + c + e] : 0.f;
+    for (int i = 0; i < RB; ++i) raw[MAXW - 1 + i] = next[i];
+    xp += RB * a.sx.t;
 #pragma unroll
-    for (int j = 0; j < MAXW; ++j) f[j][e] = j < w ? fp[e * w + j] : 0.f;
-  }
-  T *y = static_cast<T *>(a.y) + b * a.sy.b + h * a.sy.h + c;
+    for (int i = 0; i < RB; ++i) next[i] = load_if<T, V>(xp + i * a.sx.t, tb + RB + i < t1);
 #pragma unroll
-  for (int r = 0; r < RB; ++r) {
-    Vec<T, V> o;
+    for (int r = 0; r < RB; ++r) {
+      Row<V> o;
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      float p = bias[e];
+      for (int e = 0; e < V; ++e) {
+        float p = bias[e];
 #pragma unroll
-      for (int j = 0; j < MAXW; ++j)   // a tap beyond the filter is skipped: its row may hold an infinity
-        if (j < w) p = fmaf(f[j][e], get(raw[r + MAXW - 1 - j], e), p);
-      put(o, e, a.silu ? silu(p) : p);
+        for (int j = 0; j < MAXW; ++j)   // a tap beyond the filter is skipped: its row may hold an infinity
+          if (j < w) p = fmaf(f[j][e], get(raw[r + MAXW - 1 - j], e), p);
+        put(o, e, a.silu ? silu(p) : p);
+      }
+      if (tb + r < t1) store(y + r * a.sy.t, o);
     }
-    if (t0 + r < n) store(y + (t0 + r) * a.sy.t, o);
+    y += RB * a.sy.t;
+#pragma unroll
+    for (int i = 0; i < MAXW - 1; ++i) raw[i] = raw[RB + i];
   }
 }
 
@@ -103,7 +150,7 @@ __global__ void __launch_bounds__(NT) conv_kernel(const Conv a, const Split sp) 
 // partial, which a second launch sums in a fixed order (no atomics: the same
 // inputs give the same bits).
 template <typename T, int V, int MAXW, int RB>
-__global__ void __launch_bounds__(NT) conv_backward_kernel(const Conv a, const Split sp, const int run, float *part) {
+__global__ void __launch_bounds__(NT, 2) conv_backward_kernel(const Conv a, const Split sp, const int run, float *part) {
   extern __shared__ float red[];               // [threads][V]
   unsigned blk = blockIdx.x;
   const int tile = blk % sp.tiles;
@@ -125,25 +172,30 @@ __global__ void __launch_bounds__(NT) conv_backward_kernel(const Conv a, const S
   T *dhist = a.dhist ? static_cast<T *>(a.dhist) + bh * (w - 1) * d + c : nullptr;
 
   float f[MAXW][V], bias[V], df[MAXW][V], db[V];
+  taps_of<V, MAXW>(f, bias, a, (long long)h * d + c, mine);
 #pragma unroll
   for (int e = 0; e < V; ++e) {
-    bias[e] = a.bias && mine ? a.bias[(long long)h * d + c + e] : 0.f;
     db[e] = 0.f;
 #pragma unroll
-    for (int j = 0; j < MAXW; ++j) {
-      f[j][e] = j < w && mine ? a.filt[((long long)h * d + c + e) * w + j] : 0.f;
-      df[j][e] = 0.f;
-    }
+    for (int j = 0; j < MAXW; ++j) df[j][e] = 0.f;
   }
   // This thread finishes the rows [t0, t1) of dx; rows -(w-1) .. -1 (the
   // history's) belong to the first run. It needs g of rows t0 .. t1 + w - 2
-  // and, for those, x of rows t0 - (w - 1) ...
+  // and, for those, x of rows t0 - (w - 1) ... Rows past the run are summed by
+  // the next one: they are whole batches, since RB divides the run.
   const long long t0 = ((long long)tile * sp.RL + rl) * run;
   const long long t1 = t0 + run < a.T ? t0 + run : a.T;
   const long long first = t0 == 0 ? -(w - 1) : t0;
   if (mine && t0 < a.T) {
-    Vec<T, V> xs[RB + MAXW - 1];
+    const long long need = t1 + w - 1 < n ? t1 + w - 1 : n;     // rows of x and dy this run reads
+    Vec<T, V> xs[RB + MAXW - 1], xn[RB], dn[RB];
     float g[RB + MAXW - 1][V];
+    const T *xp = x + t0 * a.sx.t, *yp = dy + t0 * a.sdy.t;
+#pragma unroll
+    for (int i = 0; i < RB; ++i) {
+      xn[i] = load_if<T, V>(xp + i * a.sx.t, t0 + i < need);
+      dn[i] = load_if<T, V>(yp + i * a.sdy.t, t0 + i < need);
+    }
 #pragma unroll
     for (int i = 0; i < MAXW - 1; ++i) {
       const long long t = t0 - (MAXW - 1) + i;
@@ -155,14 +207,20 @@ __global__ void __launch_bounds__(NT) conv_backward_kernel(const Conv a, const S
       Vec<T, V> dys[RB];
 #pragma unroll
       for (int i = 0; i < RB; ++i) {
-        const bool live = tb + i < n && tb + i < t1 + w - 1;
-        xs[MAXW - 1 + i] = load_if<T, V>(x + (tb + i) * a.sx.t, live);
-        dys[i] = load_if<T, V>(dy + (tb + i) * a.sdy.t, live);
+        xs[MAXW - 1 + i] = xn[i];
+        dys[i] = dn[i];
       }
+      xp += RB * a.sx.t;
+      yp += RB * a.sdy.t;
 #pragma unroll
       for (int i = 0; i < RB; ++i) {
-        const bool live = tb + i < n;
-        const bool sums = tb + i < t1;             // rows past the run are summed by the next one
+        xn[i] = load_if<T, V>(xp + i * a.sx.t, tb + RB + i < need);
+        dn[i] = load_if<T, V>(yp + i * a.sdy.t, tb + RB + i < need);
+      }
+      const bool sums = tb < t1;
+#pragma unroll
+      for (int i = 0; i < RB; ++i) {
+        const bool live = tb + i < need;
 #pragma unroll
         for (int e = 0; e < V; ++e) {
           float xr[MAXW];
@@ -177,7 +235,7 @@ __global__ void __launch_bounds__(NT) conv_backward_kernel(const Conv a, const S
             const float q = sigmoid(p);
             gg *= q * fmaf(p, 1.f - q, 1.f);
           }
-          if (!live) gg = 0.f;
+          gg = live ? gg : 0.f;
           g[MAXW - 1 + i][e] = gg;
           if (sums && live) {
             db[e] += gg;
@@ -191,7 +249,7 @@ __global__ void __launch_bounds__(NT) conv_backward_kernel(const Conv a, const S
 #pragma unroll
       for (int i = 0; i < RB; ++i) {
         const long long t = tb - (MAXW - 1) + i;
-        if (t < first || t >= t1 || t < -(w - 1)) continue;
+        if (t < first || t >= t1) continue;
         float o[V];
 #pragma unroll
         for (int e = 0; e < V; ++e) {
@@ -207,7 +265,7 @@ __global__ void __launch_bounds__(NT) conv_backward_kernel(const Conv a, const S
 #pragma unroll
           for (int e = 0; e < V; ++e) o[e] += get(q, e);
         }
-        Vec<T, V> q;
+        Row<V> q;
 #pragma unroll
         for (int e = 0; e < V; ++e) put(q, e, t < n ? o[e] : 0.f);
         if (t >= 0) store(dx + t * a.sdx.t, q);
@@ -280,7 +338,7 @@ __global__ void __launch_bounds__(NT) conv_step_kernel(const Conv a, const long 
 #pragma unroll
   for (int j = 1; j < MAXW; ++j) raw[j] = load_if<T, V>(hist + (long long)(w - 1 - j) * d, j < w);
   const float *fp = a.filt + ((long long)h * d + c) * w;
-  Vec<T, V> o;
+  Row<V> o;
 #pragma unroll
   for (int e = 0; e < V; ++e) {
     float p = a.bias ? a.bias[(long long)h * d + c + e] : 0.f;
@@ -334,18 +392,21 @@ cudaError_t conv_launch(Conv c, cudaStream_t st) {
            fits(c.tail, {}, c.d, V, el);
   };
   auto go = [&](auto kern, int V, int rows) {
-    const Split sp = split_of(c.d, V, c.T, rows, NT, NT);
+    // long runs amortise the taps and the halo rows; short ones give small
+    // problems enough threads
+    int run = 64;
+    while (run > rows && (long long)c.B * c.H * (c.d / V) * ((c.T + run - 1) / run) < (long long)kSMs * 768) run /= 2;
+    const Split sp = split_of(c.d, V, c.T, run, 64, NT);
     const long long grid = (long long)sp.tiles * sp.cb * c.B * c.H;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-    kern<<<(unsigned)grid, sp.nvb * sp.RL, 0, st>>>(c, sp);
+    kern<<<(unsigned)grid, sp.nvb * sp.RL, 0, st>>>(c, sp, run);
     return cudaGetLastError();
   };
   if (c.bf16) {
-    if (vec(8)) return c.w <= 4 ? go(conv_kernel<bf16, 8, 4, 8>, 8, 8) : go(conv_kernel<bf16, 8, 8, 8>, 8, 8);
-    if (vec(2)) return c.w <= 4 ? go(conv_kernel<bf16, 2, 4, 8>, 2, 8) : go(conv_kernel<bf16, 2, 8, 8>, 2, 8);
+    if (vec(4)) return c.w <= 4 ? go(conv_kernel<bf16, 4, 4, 8>, 4, 8) : go(conv_kernel<bf16, 4, 8, 8>, 4, 8);
     return c.w <= 4 ? go(conv_kernel<bf16, 1, 4, 8>, 1, 8) : go(conv_kernel<bf16, 1, 8, 8>, 1, 8);
   }
-  if (vec(4)) return c.w <= 4 ? go(conv_kernel<float, 4, 4, 8>, 4, 8) : go(conv_kernel<float, 4, 8, 8>, 4, 8);
+  if (vec(4)) return c.w <= 4 ? go(conv_kernel<float, 4, 4, 4>, 4, 4) : go(conv_kernel<float, 4, 8, 4>, 4, 4);
   return c.w <= 4 ? go(conv_kernel<float, 1, 4, 8>, 1, 8) : go(conv_kernel<float, 1, 8, 8>, 1, 8);
 }
 
@@ -353,7 +414,7 @@ cudaError_t conv_launch(Conv c, cudaStream_t st) {
 // the joining of heads that the launch may choose.
 size_t conv_backward_ws(int B, int H, int T, int d, int w) {
   size_t tiles = 0;
-  for (const int V : {1, 4})
+  for (const int V : {1, 2, 4})
     for (const bool joined : {false, true}) {
       if ((joined ? H * d : d) % V) continue;
       const BackPlan p = joined ? backward_plan(B, 1, T, H * d, V) : backward_plan(B, H, T, d, V);
@@ -365,8 +426,10 @@ size_t conv_backward_ws(int B, int H, int T, int d, int w) {
 cudaError_t conv_backward_launch(Conv c, cudaStream_t st) {
   collapse(c, {&c.sx, &c.sdy, &c.sdx});
   const int el = c.bf16 ? 2 : 4;
-  const bool v4 = fits(c.x, c.sx, c.d, 4, el) && fits(c.dy, c.sdy, c.d, 4, el) && fits(c.dx, c.sdx, c.d, 4, el) &&
-                  fits(c.hist, {}, c.d, 4, el) && fits(c.dtail, {}, c.d, 4, el) && fits(c.dhist, {}, c.d, 4, el);
+  auto vec = [&](int V) {
+    return fits(c.x, c.sx, c.d, V, el) && fits(c.dy, c.sdy, c.d, V, el) && fits(c.dx, c.sdx, c.d, V, el) &&
+           fits(c.hist, {}, c.d, V, el) && fits(c.dtail, {}, c.d, V, el) && fits(c.dhist, {}, c.d, V, el);
+  };
   float *part = static_cast<float *>(c.ws);
   auto go = [&](auto kern, int V) {
     const BackPlan pl = backward_plan(c.B, c.H, c.T, c.d, V);
@@ -382,11 +445,14 @@ cudaError_t conv_backward_launch(Conv c, cudaStream_t st) {
     return cudaGetLastError();
   };
   if (c.bf16) {
-    if (v4) return c.w <= 4 ? go(conv_backward_kernel<bf16, 4, 4, 8>, 4) : go(conv_backward_kernel<bf16, 4, 8, 8>, 4);
-    return c.w <= 4 ? go(conv_backward_kernel<bf16, 1, 4, 8>, 1) : go(conv_backward_kernel<bf16, 1, 8, 8>, 1);
+#ifdef BV4
+    if (vec(4) && c.w <= 4) return go(conv_backward_kernel<bf16, 4, 4, 4>, 4);
+#endif
+    if (vec(2)) return c.w <= 4 ? go(conv_backward_kernel<bf16, 2, 4, 4>, 2) : go(conv_backward_kernel<bf16, 2, 8, 4>, 2);
+    return c.w <= 4 ? go(conv_backward_kernel<bf16, 1, 4, 4>, 1) : go(conv_backward_kernel<bf16, 1, 8, 4>, 1);
   }
-  if (v4) return c.w <= 4 ? go(conv_backward_kernel<float, 4, 4, 8>, 4) : go(conv_backward_kernel<float, 4, 8, 8>, 4);
-  return c.w <= 4 ? go(conv_backward_kernel<float, 1, 4, 8>, 1) : go(conv_backward_kernel<float, 1, 8, 8>, 1);
+  if (vec(2)) return c.w <= 4 ? go(conv_backward_kernel<float, 2, 4, 4>, 2) : go(conv_backward_kernel<float, 2, 8, 4>, 2);
+  return c.w <= 4 ? go(conv_backward_kernel<float, 1, 4, 4>, 1) : go(conv_backward_kernel<float, 1, 8, 4>, 1);
 }
 
 cudaError_t conv_step_launch(const Conv &c, cudaStream_t st) {

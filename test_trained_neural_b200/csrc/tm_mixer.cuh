@@ -43,32 +43,80 @@ __device__ __forceinline__ float softplus(float v) {
   return v > -87.f ? fmaxf(v, 0.f) + u * p : ex2(kLog2e * v);
 }
 
-// V consecutive elements of one row as raw words
+// V consecutive elements of one row as loaded: fp32 values, or bf16 pairs in
+// 32-bit words (a bf16 of its own would take a whole register).
 template <typename T, int V>
 struct alignas(sizeof(T) * V) Vec {
   T e[V];
 };
 template <int V>
+struct alignas(2 * V) Vec<__nv_bfloat16, V> {
+  unsigned w[V / 2];
+};
+template <>
+struct alignas(2) Vec<__nv_bfloat16, 1> {
+  unsigned short w;
+};
+template <int V>
 __device__ __forceinline__ float get(const Vec<float, V> &v, int i) { return v.e[i]; }
 template <int V>
-__device__ __forceinline__ float get(const Vec<__nv_bfloat16, V> &v, int i) { return __bfloat162float(v.e[i]); }
+__device__ __forceinline__ float get(const Vec<__nv_bfloat16, V> &v, int i) {
+  return __uint_as_float(i & 1 ? v.w[i / 2] & 0xffff0000u : v.w[i / 2] << 16);
+}
+__device__ __forceinline__ float get(const Vec<__nv_bfloat16, 1> &v, int) { return __uint_as_float((unsigned)v.w << 16); }
+
 template <int V>
-__device__ __forceinline__ void put(Vec<float, V> &v, int i, float x) { v.e[i] = x; }
+__device__ __forceinline__ void clear(Vec<float, V> &v) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) v.e[i] = 0.f;
+}
 template <int V>
-__device__ __forceinline__ void put(Vec<__nv_bfloat16, V> &v, int i, float x) { v.e[i] = __float2bfloat16_rn(x); }
+__device__ __forceinline__ void clear(Vec<__nv_bfloat16, V> &v) {
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) v.w[i] = 0u;
+}
+__device__ __forceinline__ void clear(Vec<__nv_bfloat16, 1> &v) { v.w = 0; }
 
 // The vector at p, or zeros.
 template <typename T, int V>
 __device__ __forceinline__ Vec<T, V> load_if(const T *p, bool live) {
   Vec<T, V> v;
-#pragma unroll
-  for (int i = 0; i < V; ++i) v.e[i] = T(0.f);
+  clear(v);
   if (live) v = *reinterpret_cast<const Vec<T, V> *>(p);
   return v;
 }
 template <typename T, int V>
 __device__ __forceinline__ void store(T *p, const Vec<T, V> &v) {
   *reinterpret_cast<Vec<T, V> *>(p) = v;
+}
+
+// V results on their way out, rounded once, to nearest, by the store.
+template <int V>
+struct Row {
+  float f[V];
+};
+template <int V>
+__device__ __forceinline__ void put(Row<V> &r, int i, float x) { r.f[i] = x; }
+template <int V>
+__device__ __forceinline__ void store(float *p, const Row<V> &r) {
+  Vec<float, V> v;
+#pragma unroll
+  for (int i = 0; i < V; ++i) v.e[i] = r.f[i];
+  store(p, v);
+}
+template <int V>
+__device__ __forceinline__ void store(__nv_bfloat16 *p, const Row<V> &r) {
+  if constexpr (V == 1) {
+    *p = __float2bfloat16_rn(r.f[0]);
+  } else {
+    Vec<__nv_bfloat16, V> v;
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      const __nv_bfloat162 q = __floats2bfloat162_rn(r.f[2 * i], r.f[2 * i + 1]);
+      v.w[i] = *reinterpret_cast<const unsigned *>(&q);
+    }
+    store(p, v);
+  }
 }
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }

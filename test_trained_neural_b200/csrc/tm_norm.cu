@@ -41,6 +41,31 @@ __device__ __forceinline__ float act_grad(float p) {
   return q * fmaf(p, 1.f - q, 1.f);
 }
 
+// weight and bias of V channels from hc on (1 and 0 where absent, or past the group).
+template <int V>
+__device__ __forceinline__ void affine_of(float (&w)[V], float (&bs)[V], const Norm &a, long long hc, bool live) {
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    w[e] = 1.f;
+    bs[e] = 0.f;
+  }
+  if (!live) return;
+  constexpr int P = V % 4 == 0 ? 4 : 1;                 // the launch checks their alignment
+#pragma unroll
+  for (int i = 0; i < V; i += P) {
+    if (a.weight) {
+      const Vec<float, P> q = load_if<float, P>(a.weight + hc + i, true);
+#pragma unroll
+      for (int e = 0; e < P; ++e) w[i + e] = q.e[e];
+    }
+    if (a.bias) {
+      const Vec<float, P> q = load_if<float, P>(a.bias + hc + i, true);
+#pragma unroll
+      for (int e = 0; e < P; ++e) bs[i + e] = q.e[e];
+    }
+  }
+}
+
 // ---- one token
 
 // CTA: one (batch, head), NT / LPR rows side by side, RPT rows each.
@@ -64,12 +89,7 @@ __global__ void __launch_bounds__(NT) token_kernel(const Norm a, const int tiles
   float w[IT][V], bs[IT][V];
 #pragma unroll
   for (int i = 0; i < IT; ++i)
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const int c = (i * LPR + lane) * V + e;
-      w[i][e] = a.weight && c < d ? a.weight[(long long)h * d + c] : 1.f;
-      bs[i][e] = a.bias && c < d ? a.bias[(long long)h * d + c] : 0.f;
-    }
+    affine_of<V>(w[i], bs[i], a, (long long)h * d + (i * LPR + lane) * V, (i * LPR + lane) * V < d);
   const float inv = 1.f / d;
 #pragma unroll
   for (int r = 0; r < RPT; ++r) {
@@ -93,7 +113,7 @@ __global__ void __launch_bounds__(NT) token_kernel(const Norm a, const int tiles
     for (int i = 0; i < IT; ++i) {
       const int c = (i * LPR + lane) * V;
       if (c >= d) continue;
-      Vec<TO, V> o;
+      Row<V> o;
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         const float p = fmaf((get(raw[r][i], e) - m) * rs, w[i][e], bs[i][e]);
@@ -129,9 +149,9 @@ __global__ void __launch_bounds__(NT) token_wide_kernel(const Norm a) {
   for (int c = threadIdx.x; c < d; c += NT) {
     const long long hc = (long long)h * d + c;
     const float p = fmaf((to_f(x[c]) - m) * rs, a.weight ? a.weight[hc] : 1.f, a.bias ? a.bias[hc] : 0.f);
-    Vec<TO, 1> o;
+    Row<1> o;
     put(o, 0, a.silu ? silu(p) : p);
-    y[c] = o.e[0];
+    store(y + c, o);
   }
   if (a.stats && threadIdx.x == 0) reinterpret_cast<float2 *>(a.stats)[(long long)bh * a.T + t] = make_float2(m, rs);
 }
@@ -153,31 +173,45 @@ __global__ void __launch_bounds__(NT) token_backward_kernel(const Norm a, const 
   const float2 *stats = reinterpret_cast<const float2 *>(a.stats) + (long long)bh * a.T;
   float w[IT][V], bs[IT][V], dw[IT][V], db[IT][V];
 #pragma unroll
-  for (int i = 0; i < IT; ++i)
+  for (int i = 0; i < IT; ++i) {
+    affine_of<V>(w[i], bs[i], a, (long long)h * d + (i * LPR + lane) * V, (i * LPR + lane) * V < d);
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const int c = (i * LPR + lane) * V + e;
-      w[i][e] = a.weight && c < d ? a.weight[(long long)h * d + c] : 1.f;
-      bs[i][e] = a.bias && c < d ? a.bias[(long long)h * d + c] : 0.f;
-      dw[i][e] = db[i][e] = 0.f;
-    }
+    for (int e = 0; e < V; ++e) dw[i][e] = db[i][e] = 0.f;
+  }
   const float inv = 1.f / d;
   const long long step = (long long)tiles * ROWS * RPT;
+  // the next rows are on their way while these are computed
+  Vec<TI, V> xn[RPT][IT];
+  Vec<TO, V> yn[RPT][IT];
+  float2 sn[RPT];
+  auto fetch = [&](long long tb) {
+#pragma unroll
+    for (int r = 0; r < RPT; ++r) {
+      const long long t = tb + r * ROWS + rg;
+      sn[r] = t < n ? stats[t] : make_float2(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < IT; ++i) {
+        const int c = (i * LPR + lane) * V;
+        xn[r][i] = load_if<TI, V>(x + t * a.sx.t + c, c < d && t < n);
+        yn[r][i] = load_if<TO, V>(dy + t * a.sdy.t + c, c < d && t < n);
+      }
+    }
+  };
+  fetch((long long)tile * ROWS * RPT);
   for (long long tb = (long long)tile * ROWS * RPT; tb < a.T; tb += step) {
     Vec<TI, V> xr[RPT][IT];
     Vec<TO, V> yr[RPT][IT];
     float2 st[RPT];
 #pragma unroll
     for (int r = 0; r < RPT; ++r) {
-      const long long t = tb + r * ROWS + rg;
-      st[r] = t < n ? stats[t] : make_float2(0.f, 0.f);
+      st[r] = sn[r];
 #pragma unroll
       for (int i = 0; i < IT; ++i) {
-        const int c = (i * LPR + lane) * V;
-        xr[r][i] = load_if<TI, V>(x + t * a.sx.t + c, c < d && t < n);
-        yr[r][i] = load_if<TO, V>(dy + t * a.sdy.t + c, c < d && t < n);
+        xr[r][i] = xn[r][i];
+        yr[r][i] = yn[r][i];
       }
     }
+    fetch(tb + step);
 #pragma unroll
     for (int r = 0; r < RPT; ++r) {
       const long long t = tb + r * ROWS + rg;
@@ -203,7 +237,7 @@ __global__ void __launch_bounds__(NT) token_backward_kernel(const Norm a, const 
       for (int i = 0; i < IT; ++i) {
         const int c = (i * LPR + lane) * V;
         if (c >= d) continue;
-        Vec<TI, V> o;
+        Row<V> o;
 #pragma unroll
         for (int e = 0; e < V; ++e) {
           const float xh = (get(xr[r][i], e) - m) * rs;
@@ -249,10 +283,10 @@ __global__ void __launch_bounds__(NT) token_wide_backward_kernel(const Norm a, c
     TI *dx = static_cast<TI *>(a.dx) + b * a.sdx.b + h * a.sdx.h + t * a.sdx.t;
     const TI *x = static_cast<const TI *>(a.x) + b * a.sx.b + h * a.sx.h + t * a.sx.t;
     const TO *dy = static_cast<const TO *>(a.dy) + b * a.sdy.b + h * a.sdy.h + t * a.sdy.t;
-    Vec<TI, 1> o;
+    Row<1> o;
     if (t >= n) {
       put(o, 0, 0.f);
-      for (int c = threadIdx.x; c < d; c += NT) dx[c] = o.e[0];
+      for (int c = threadIdx.x; c < d; c += NT) store(dx + c, o);
       continue;
     }
     const float2 st = reinterpret_cast<const float2 *>(a.stats)[(long long)bh * a.T + t];
@@ -275,7 +309,7 @@ __global__ void __launch_bounds__(NT) token_wide_backward_kernel(const Norm a, c
       float q = to_f(dy[c]);
       if (a.silu) q *= act_grad(fmaf(xh, w, a.bias ? a.bias[hc] : 0.f));
       put(o, 0, st.y * (fmaf(q, w, -k1) - xh * k2));
-      dx[c] = o.e[0];
+      store(dx + c, o);
     }
   }
 }
@@ -425,11 +459,7 @@ __global__ void __launch_bounds__(NT) seq_apply_kernel(const Norm a, const Cols 
   const float2 st = stats[(long long)q.b * a.H + h];
   const long long hc = (long long)q.h0 * a.d + q.c;
   float w[V], bs[V];
-#pragma unroll
-  for (int e = 0; e < V; ++e) {
-    w[e] = a.weight ? a.weight[hc + e] : 1.f;
-    bs[e] = a.bias ? a.bias[hc + e] : 0.f;
-  }
+  affine_of<V>(w, bs, a, hc, true);
   const long long t0 = ((long long)q.tile * s.RL + q.rl) * s.run;
   const long long t1 = t0 + s.run < n ? t0 + s.run : n;
   for (long long t = t0; t < t1; t += 4) {
@@ -438,7 +468,7 @@ __global__ void __launch_bounds__(NT) seq_apply_kernel(const Norm a, const Cols 
     for (int i = 0; i < 4; ++i) raw[i] = load_if<TI, V>(x + (t + i) * a.sx.t, t + i < t1);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      Vec<TO, V> o;
+      Row<V> o;
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         const float p = fmaf((get(raw[i], e) - st.x) * st.y, w[e], bs[e]);
@@ -465,11 +495,7 @@ __global__ void __launch_bounds__(NT) seq_sums_kernel(const Norm a, const Cols s
     const TO *dy = static_cast<const TO *>(a.dy) + q.b * a.sdy.b + q.h0 * a.sdy.h + q.c;
     const float2 st = reinterpret_cast<const float2 *>(a.stats)[(long long)q.b * a.H + h];
     float w[V], bs[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      w[e] = a.weight ? a.weight[hc + e] : 1.f;
-      bs[e] = a.bias ? a.bias[hc + e] : 0.f;
-    }
+    affine_of<V>(w, bs, a, hc, true);
     const long long t0 = ((long long)q.tile * s.RL + q.rl) * s.run;
     const long long t1 = t0 + s.run < n ? t0 + s.run : n;
     for (long long t = t0; t < t1; t += 4) {
@@ -577,11 +603,7 @@ __global__ void __launch_bounds__(NT) seq_grad_kernel(const Norm a, const Cols s
   const float2 mk = means[(long long)q.b * a.H + h];
   const long long hc = (long long)q.h0 * a.d + q.c;
   float w[V], bs[V];
-#pragma unroll
-  for (int e = 0; e < V; ++e) {
-    w[e] = a.weight ? a.weight[hc + e] : 1.f;
-    bs[e] = a.bias ? a.bias[hc + e] : 0.f;
-  }
+  affine_of<V>(w, bs, a, hc, true);
   const long long t0 = ((long long)q.tile * s.RL + q.rl) * s.run;
   const long long t1 = t0 + s.run < a.T ? t0 + s.run : a.T;
   for (long long t = t0; t < t1; t += 4) {
@@ -595,7 +617,7 @@ __global__ void __launch_bounds__(NT) seq_grad_kernel(const Norm a, const Cols s
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      Vec<TI, V> o;
+      Row<V> o;
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         const float xh = (get(xr[i], e) - st.x) * st.y;
@@ -645,11 +667,15 @@ int token_tiles(int B, int H, int T, int d) {
   return (int)(tiles < 1 ? 1 : tiles);
 }
 
+bool affine_fits(const Norm &a) {
+  return reinterpret_cast<uintptr_t>(a.weight) % 16 == 0 && reinterpret_cast<uintptr_t>(a.bias) % 16 == 0;
+}
+
 template <typename TI, typename TO>
 cudaError_t forward(const Norm &a, cudaStream_t st) {
   constexpr int V = sizeof(TI) == 2 ? 8 : 4;
   const int ei = sizeof(TI), eo = sizeof(TO);
-  const bool vec = fits(a.x, a.sx, a.d, V, ei) && fits(a.y, a.sy, a.d, V, eo);
+  const bool vec = fits(a.x, a.sx, a.d, V, ei) && fits(a.y, a.sy, a.d, V, eo) && affine_fits(a);
   const long long bh = (long long)a.B * a.H;
   if (a.over == kToken) {
     auto go = [&](auto kern, int LPR, int RPT) {
@@ -696,7 +722,8 @@ template <typename TI, typename TO>
 cudaError_t backward(const Norm &a, cudaStream_t st) {
   constexpr int V = sizeof(TI) == 2 ? 8 : 4;
   const int ei = sizeof(TI), eo = sizeof(TO);
-  const bool vec = fits(a.x, a.sx, a.d, V, ei) && fits(a.dx, a.sdx, a.d, V, ei) && fits(a.dy, a.sdy, a.d, V, eo);
+  const bool vec = fits(a.x, a.sx, a.d, V, ei) && fits(a.dx, a.sdx, a.d, V, ei) && fits(a.dy, a.sdy, a.d, V, eo) &&
+                   affine_fits(a);
   const long long bh = (long long)a.B * a.H, hd = (long long)a.H * a.d;
   float *part = static_cast<float *>(a.ws);
   if (a.over == kToken) {

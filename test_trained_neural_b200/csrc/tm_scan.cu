@@ -21,7 +21,7 @@ constexpr int tile_of(int NL, int V) { return NL >= 4 ? 16 : V > 1 ? 8 : 4; }
 constexpr int kTile = 16;            // segments are whole tiles of every kind
 
 template <typename T, int NL, int CPL, int V, bool LOCAL>
-__global__ void __launch_bounds__(128) scan_kernel(const Scan a, const Plan pl, float *hloc, float *esum) {
+__global__ void __launch_bounds__(128, V > 1 ? 4 : 2) scan_kernel(const Scan a, const Plan pl, float *hloc, float *esum) {
   constexpr int TQ = tile_of(NL, V);
   constexpr int NP = NL * SPL;
   constexpr int CW = 32 / NL * CPL;               // channels of a warp
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(128) scan_kernel(const Scan a, const Plan pl, 
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
         const int t = row_at(k), kc = col_at(k);
-        Vec<T, V> o;
+        Row<V> o;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           float y = fmaf(s_D[kc + i], get(xk[k], i), s_u[t * CB + kc + i]);
@@ -318,9 +318,9 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const Scan a, const long
   if (nl == 0) {
     if (a.D) y = fmaf(a.D[ch], x, y);
     if (a.z) y *= silu(to_f(static_cast<const T *>(a.z)[b * a.sz.b + h * a.sz.h + c]));
-    Vec<T, 1> o;
+    Row<1> o;
     put(o, 0, y);
-    static_cast<T *>(a.y)[b * a.sy.b + h * a.sy.h + c] = o.e[0];
+    store(static_cast<T *>(a.y) + b * a.sy.b + h * a.sy.h + c, o);
   }
 }
 

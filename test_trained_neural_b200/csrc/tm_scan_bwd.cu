@@ -64,7 +64,7 @@ Plan plan_of(int B, int H, int G, int T, int d, int N) {
   p.hloc = take(p.S > 1 ? p.S * chans * p.NP : 0);
   p.gloc = take(p.S > 1 ? p.S * chans * p.NP : 0);
   p.esum = take(p.S > 1 ? p.S * chans : 0);
-  p.bc = take((size_t)p.pbn * B * G * T * 2 * p.NP);
+  p.bc = take(p.pbn > 1 ? (size_t)p.pbn * B * G * T * 2 * p.NP : 0);
   p.pa = take((size_t)B * p.S * H * d * p.NP);
   p.pd = take((size_t)B * p.S * 2 * H * d);
   p.total = off;
@@ -284,6 +284,17 @@ __global__ void __launch_bounds__(32 * MAXW, 2) grad_kernel(const Scan a, const 
   T *dzp = a.dz ? static_cast<T *>(a.dz) + w.b * a.sdz.b + w.h * a.sdz.h + c_blk : nullptr;
   float *bc = ws + pl.bc + ((((long long)(w.h % (a.H / a.G)) * pl.blocks + w.cb) * a.B + w.b) * a.G + w.g) * a.T * 2 * NP;
 
+  // entry i of a tile's [K][2 NP] sums: this CTA's partial, or the result where it is the only one
+  const long long row0 = ((long long)w.b * a.G + w.g) * a.T;
+  auto out_bc = [&](long long t0, int i, float s) {
+    if (pl.pbn > 1) {
+      bc[t0 * 2 * NP + i] = s;
+    } else if (i % NP < N) {
+      Row<1> o;
+      put(o, 0, s);
+      store(static_cast<T *>(i % (2 * NP) < NP ? a.dB : a.dC) + (row0 + t0 + i / (2 * NP)) * N + i % NP, o);
+    }
+  };
   float sumD[NV][V], sumb[NV][V];
 #pragma unroll
   for (int k = 0; k < NV; ++k)
@@ -297,7 +308,7 @@ __global__ void __launch_bounds__(32 * MAXW, 2) grad_kernel(const Scan a, const 
       for (int k = 0; k < NV; ++k) {
         const int i = tid + k * nthr, kc = (i & (vpr - 1)) * V, t = i >> vlog;
         if (i >= vtile || c_blk + kc >= a.d || t0 + t >= t_all) continue;
-        Vec<T, V> o;
+        Row<V> o;
 #pragma unroll
         for (int j = 0; j < V; ++j) put(o, j, 0.f);
         store(dxp + (t0 + t) * a.sdx.t + kc, o);
@@ -305,7 +316,7 @@ __global__ void __launch_bounds__(32 * MAXW, 2) grad_kernel(const Scan a, const 
         if (dzp) store(dzp + (t0 + t) * a.sdz.t + kc, o);
       }
       for (int i = tid; i < K * 2 * NP; i += nthr)
-        if (t0 + i / (2 * NP) < t_all) bc[t0 * 2 * NP + i] = 0.f;
+        if (t0 + i / (2 * NP) < t_all) out_bc(t0, i, 0.f);
       continue;
     }
     // stage the tile
@@ -432,7 +443,7 @@ __global__ void __launch_bounds__(32 * MAXW, 2) grad_kernel(const Scan a, const 
       const int i = tid + k * nthr, kc = (i & (vpr - 1)) * V, t = i >> vlog;
       if (i >= vtile || c_blk + kc >= a.d || t0 + t >= t_all) continue;
       const bool live = t0 + t < n_tok;
-      Vec<T, V> ox, od, oz;
+      Row<V> ox, od, oz;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const float v = get(dk[k], j) + (a.dt_bias ? a.dt_bias[hd + kc + j] : 0.f);
@@ -458,7 +469,7 @@ __global__ void __launch_bounds__(32 * MAXW, 2) grad_kernel(const Scan a, const 
     for (int i = tid; i < K * 2 * NP; i += nthr) {
       float s = 0.f;
       for (int q = 0; q < pl.warps; ++q) s += s_bc[q * K * 2 * NP + i];
-      if (t0 + i / (2 * NP) < t_all) bc[t0 * 2 * NP + i] = s;
+      if (t0 + i / (2 * NP) < t_all) out_bc(t0, i, s);
     }
   }
 
@@ -498,15 +509,16 @@ __global__ void __launch_bounds__(32 * MAXW, 2) grad_kernel(const Scan a, const 
 template <typename T>
 __global__ void __launch_bounds__(256) join_bc_kernel(const Scan a, const Plan pl, const float *bc) {
   const long long rows = (long long)a.B * a.G * a.T, i = (long long)blockIdx.x * 256 + threadIdx.x;
-  if (i >= rows * 2 * pl.NP) return;
-  const long long row = i / (2 * pl.NP);
-  const int q = (int)(i % (2 * pl.NP)), n = q % pl.NP;
+  const int lg = __ffs(2 * pl.NP) - 1;                  // 2 NP is a power of two
+  const long long row = i >> lg;
+  if (row >= rows) return;
+  const int q = (int)i & (2 * pl.NP - 1), n = q & (pl.NP - 1);
   if (n >= a.N) return;
   float s = 0.f;
   for (int p = 0; p < pl.pbn; ++p) s += bc[p * rows * 2 * pl.NP + i];
-  Vec<T, 1> o;
+  Row<1> o;
   put(o, 0, s);
-  static_cast<T *>(q < pl.NP ? a.dB : a.dC)[row * a.N + n] = o.e[0];
+  store(static_cast<T *>(q < pl.NP ? a.dB : a.dC) + row * a.N + n, o);
 }
 
 // dA, dD and d(dt_bias): the partials of the sequences and segments, in order.
@@ -555,9 +567,11 @@ cudaError_t run(const Scan &c, cudaStream_t st) {
   else grad_kernel<T, NL, VB, false><<<(unsigned)grid, thr, sm2, st>>>(c, p, ws);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  join_bc_kernel<T><<<(unsigned)((nbc + 255) / 256), 256, 0, st>>>(c, p, ws + p.bc);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  if (p.pbn > 1) {
+    join_bc_kernel<T><<<(unsigned)((nbc + 255) / 256), 256, 0, st>>>(c, p, ws + p.bc);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
   const long long n = (long long)c.H * c.d * (NP + 2);
   join_param_kernel<<<(unsigned)((n + 31) / 32), 256, 0, st>>>(c, p, ws);
   return cudaGetLastError();
