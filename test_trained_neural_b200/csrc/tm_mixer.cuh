@@ -121,6 +121,74 @@ __device__ __forceinline__ void store(__nv_bfloat16 *p, const Row<V> &r) {
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 
+// V floats of shared memory, in 16-byte pieces (V a multiple of 4 or less than 4)
+template <int V>
+__device__ __forceinline__ void lds(float (&v)[V], const float *p) {
+  constexpr int P = V < 4 ? V : 4;
+#pragma unroll
+  for (int i = 0; i < V; i += P) {
+    const Vec<float, P> q = *reinterpret_cast<const Vec<float, P> *>(p + i);
+#pragma unroll
+    for (int j = 0; j < P; ++j) v[i + j] = q.e[j];
+  }
+}
+template <int V>
+__device__ __forceinline__ void sts(float *p, const float (&v)[V]) {
+  constexpr int P = V < 4 ? V : 4;
+#pragma unroll
+  for (int i = 0; i < V; i += P) {
+    Vec<float, P> q;
+#pragma unroll
+    for (int j = 0; j < P; ++j) q.e[j] = v[i + j];
+    *reinterpret_cast<Vec<float, P> *>(p + i) = q;
+  }
+}
+
+// Asynchronous copy of V elements into shared memory, zeros where not `live`
+// (nothing is read then). Pieces under 4 bytes have no asynchronous form and
+// are copied at once. A thread that reads only what it copied itself needs
+// copies_done() and no barrier.
+template <typename T, int V>
+__device__ __forceinline__ void copy_in(T *dst, const T *src, bool live) {
+  constexpr int n = sizeof(T) * V;
+  if constexpr (n >= 4) {
+    const unsigned d = (unsigned)__cvta_generic_to_shared(dst);
+    const int k = live ? n : 0;
+    if constexpr (n == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(k));
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(d), "l"(src), "n"(n), "r"(k));
+  } else {
+    store(dst, load_if<T, V>(src, live));
+  }
+}
+__device__ __forceinline__ void copies_sent() { asm volatile("cp.async.commit_group;"); }
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+
+// Two fp32 values in one 64-bit register: one instruction for both.
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 pair(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(float &a, float &b, F2 x) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x.v)); }
+__device__ __forceinline__ F2 mul(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 ex2(F2 x) {
+  float a, b;
+  unpair(a, b, x);
+  return pair(ex2(a), ex2(b));
+}
+
 // Tokens of sequence b: the caller's length held to [0, T].
 __device__ __forceinline__ int tokens_of(const int *lengths, int b, int T) {
   return lengths ? min(max(lengths[b], 0), T) : T;

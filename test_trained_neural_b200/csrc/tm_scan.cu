@@ -1,6 +1,7 @@
 // Selective state-space scan: prompts (with the sequence split over CTAs when
 // there are few channels) and single tokens. Formulas and lane layout:
 // tm_scan.cuh.
+#include <cstdlib>
 #include "tm_scan.cuh"
 
 namespace tmem {
@@ -20,17 +21,33 @@ struct Plan {
 constexpr int tile_of(int NL, int V) { return NL >= 4 ? 16 : V > 1 ? 8 : 4; }
 constexpr int kTile = 16;            // segments are whole tiles of every kind
 
-template <typename T, int NL, int CPL, int V, bool LOCAL>
-__global__ void __launch_bounds__(128, V > 1 ? 4 : 2) scan_kernel(const Scan a, const Plan pl, float *hloc, float *esum) {
-  constexpr int TQ = tile_of(NL, V);
-  constexpr int NP = NL * SPL;
-  constexpr int CW = 32 / NL * CPL;               // channels of a warp
+// Shared memory of a CTA: raw tiles of x, dt and z, twice (the next tile is on
+// its way while this one is computed); e and u = e x of the tile, u's slots
+// taking y; B and C of the tile, each value twice side by side (the operand of
+// a two-channel instruction); the bias and D of the channels.
+template <typename T, int NL, int CPL, int V, int W>
+struct Smem {
+  static constexpr int TQ = tile_of(NL, V), NP = NL * SPL, CW = 32 / NL * CPL, CB = CW * W;
+  static constexpr size_t bytes = 6 * TQ * CB * sizeof(T) + (2 * TQ * CB + 4 * TQ * NP + 2 * CB) * 4;
+};
+
+// One segment of the sequence for one block of channels; LOCAL: only the state
+// that the segment leaves from a zero (segment 0: the initial) state.
+//
+// Bound by the special-function unit: one exp per (token, channel, state) at 16
+// a clock and SM. The rest of the recurrence is written for pairs of channels
+// (fma.rn.f32x2), which halves its issue slots.
+template <typename T, int NL, int CPL, int V, int W, bool LOCAL>
+__global__ void __launch_bounds__(32 * W, (NL >= 16 ? 8 : 16) / W) scan_kernel(const Scan a, const Plan pl, float *hloc, float *esum) {
+  using S = Smem<T, NL, CPL, V, W>;
+  constexpr int TQ = S::TQ, NP = S::NP, CW = S::CW, CB = S::CB, nthr = 32 * W;
   constexpr int EPT = TQ * CW / 32;               // elements of a tile a thread stages
   constexpr int NV = EPT / V;
+  constexpr int NB = (TQ * NP + nthr - 1) / nthr; // values of B a thread stages
   extern __shared__ __align__(16) float sm[];
-  const int CB = CW * pl.warps;
-  float *s_e = sm, *s_u = s_e + TQ * CB, *s_B = s_u + TQ * CB, *s_C = s_B + TQ * NP, *s_bias = s_C + TQ * NP,
+  float *s_e = sm, *s_u = s_e + TQ * CB, *s_B = s_u + TQ * CB, *s_C = s_B + 2 * TQ * NP, *s_bias = s_C + 2 * TQ * NP,
         *s_D = s_bias + CB;
+  T *s_raw = reinterpret_cast<T *>(s_D + CB);     // [2][x, dt, z][TQ][CB]
 
   unsigned blk = blockIdx.x;
   const int segs = LOCAL ? pl.S - 1 : pl.S;
@@ -41,7 +58,6 @@ __global__ void __launch_bounds__(128, V > 1 ? 4 : 2) scan_kernel(const Scan a, 
   const int h = blk % a.H, b = blk / a.H;
   const int g = h / (a.H / a.G);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, nl = lane % NL, cl = lane / NL;
-  const int nthr = 32 * pl.warps;
   const int c_blk = cb * CB;
   const int c0 = warp * CW + cl * CPL;            // first channel of the lane, within the block
   const long long bh = (long long)b * a.H + h;
@@ -52,50 +68,12 @@ __global__ void __launch_bounds__(128, V > 1 ? 4 : 2) scan_kernel(const Scan a, 
   const long long t_seg = (long long)seg * pl.L;
   const long long t_end = t_seg + pl.L < n_tok ? t_seg + pl.L : n_tok;
 
-  for (int i = tid; i < CB; i += nthr) {
-    const bool in = c_blk + i < a.d;
-    s_bias[i] = in && a.dt_bias ? a.dt_bias[ch0 + i] : 0.f;
-    s_D[i] = in && a.D ? a.D[ch0 + i] : 0.f;
-  }
-
-  // A in base-2 exponents, and the state at the segment's start
-  float A2[CPL][SPL], hs[CPL][SPL], ehold[CPL];
-#pragma unroll
-  for (int c = 0; c < CPL; ++c) {
-    ehold[c] = 0.f;
-    const bool in = c_blk + c0 + c < a.d;
-    const long long at = (ch0 + c0 + c) * N + n0;
-#pragma unroll
-    for (int s = 0; s < SPL; ++s) {
-      const bool live = in && n0 + s < N;
-      A2[c][s] = live ? a.A[at + s] * kLog2e : 0.f;
-      hs[c][s] = 0.f;
-      if (live && a.state0 && (!LOCAL || seg == 0)) hs[c][s] = a.state0[bh * a.d * N + ((long long)(c_blk + c0 + c)) * N + n0 + s];
-    }
-  }
-  const long long per = (long long)a.B * a.H * a.d;     // channels of all streams
-  const long long chan = bh * a.d + c_blk + c0;         // the lane's first channel among them
-  if (!LOCAL && seg > 0) {
-    // join the segments before this one: what each adds from a zero state,
-    // and its decay exp(A sum e); segment 0's holds the initial state
-    for (int q = 0; q < seg; ++q)
-#pragma unroll
-      for (int c = 0; c < CPL; ++c) {
-        if (c_blk + c0 + c >= a.d) continue;
-        const float es = esum[q * per + chan + c];
-        const float *hl = hloc + (q * per + chan + c) * NP + n0;
-        const float4 v = *reinterpret_cast<const float4 *>(hl);
-        const float l[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int s = 0; s < SPL; ++s) hs[c][s] = q == 0 ? l[s] : fmaf(ex2(A2[c][s] * es), hs[c][s], l[s]);
-      }
-  }
-
   // staging: this thread's vectors of a tile are those numbered tid, tid +
-  // nthr, ...; where a row has at most nthr of them their column is fixed
-  const int vpr = CB / V, vlog = __ffs(vpr) - 1;         // vectors of a tile row, a power of two
-  auto row_at = [&](int k) { return (tid + k * nthr) >> vlog; };
-  auto col_at = [&](int k) { return CW / V <= 32 ? (tid & (vpr - 1)) * V : ((tid + k * nthr) & (vpr - 1)) * V; };
+  // nthr, ...; it copies them in, forms e and u, and writes their y
+  constexpr int vpr = CB / V;                            // vectors of a tile row
+  auto row_at = [&](int k) { return (tid + k * nthr) / vpr; };
+  auto col_at = [&](int k) { return (CW / V <= 32 ? tid : tid + k * nthr) % vpr * V; };
+  const bool idle = c_blk + warp * CW >= a.d;            // a warp beyond the head's channels only stages
   const T *xp = static_cast<const T *>(a.x) + b * a.sx.b + h * a.sx.h + c_blk;
   const T *dp = static_cast<const T *>(a.dt) + b * a.sdt.b + h * a.sdt.h + c_blk;
   const T *zp = a.z ? static_cast<const T *>(a.z) + b * a.sz.b + h * a.sz.h + c_blk : nullptr;
@@ -103,71 +81,148 @@ __global__ void __launch_bounds__(128, V > 1 ? 4 : 2) scan_kernel(const Scan a, 
   const T *Bp = static_cast<const T *>(a.Bm) + b * a.sB.b + g * a.sB.h;
   const T *Cp = static_cast<const T *>(a.Cm) + b * a.sC.b + g * a.sC.h;
 
-  Vec<T, V> xr[NV], dr[NV], zr[NV], xk[NV], zk[NV];
-  auto fetch = [&](long long t0) {
+  T Br[NB], Cr[NB];
+  auto fetch = [&](long long t0, int buf) {
+    T *raw = s_raw + buf * 3 * TQ * CB;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const long long t = t0 + row_at(k);
-      const int c = col_at(k);
+      const int r = row_at(k), c = col_at(k);
+      const long long t = t0 + r;
       const bool live = c_blk + c < a.d && t < t_end;
-      xr[k] = load_if<T, V>(xp + t * a.sx.t + c, live);
-      dr[k] = load_if<T, V>(dp + t * a.sdt.t + c, live);
-      if (!LOCAL) zr[k] = load_if<T, V>(zp + t * a.sz.t + c, live && zp);
+      T *to = raw + r * CB + c;
+      copy_in<T, V>(to, live ? xp + t * a.sx.t + c : xp, live);
+      copy_in<T, V>(to + TQ * CB, live ? dp + t * a.sdt.t + c : dp, live);
+      if (!LOCAL && zp) copy_in<T, V>(to + 2 * TQ * CB, live ? zp + t * a.sz.t + c : zp, live);
+    }
+    copies_sent();
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+      const int i = tid + k * nthr, n = i % NP;
+      const long long t = t0 + i / NP;
+      const bool live = i < TQ * NP && t < t_end && n < N;
+      Br[k] = live ? Bp[t * a.sB.t + n] : T(0.f);
+      if (!LOCAL) Cr[k] = live ? Cp[t * a.sC.t + n] : T(0.f);
     }
   };
-  fetch(t_seg);
-  const int rotate = LaneSum<CPL, NL>::first(nl);
+  fetch(t_seg, 0);
+
+  for (int i = tid; i < CB; i += nthr) {
+    const bool in = c_blk + i < a.d;
+    s_bias[i] = in && a.dt_bias ? a.dt_bias[ch0 + i] : 0.f;
+    s_D[i] = in && a.D ? a.D[ch0 + i] : 0.f;
+  }
+
+  // A in base-2 exponents, and the state at the segment's start; pairs of channels
+  constexpr int C2 = CPL / 2;
+  F2 A2[C2][SPL], hs[C2][SPL];
+  const long long per = (long long)a.B * a.H * a.d;     // channels of all streams
+  const long long chan = bh * a.d + c_blk + c0;         // the lane's first channel among them
+  {
+    float Af[CPL][SPL], hf[CPL][SPL];
+#pragma unroll
+    for (int c = 0; c < CPL; ++c) {
+      const bool in = c_blk + c0 + c < a.d;
+#pragma unroll
+      for (int s = 0; s < SPL; ++s) {
+        const bool live = in && n0 + s < N;
+        Af[c][s] = live ? a.A[(ch0 + c0 + c) * N + n0 + s] * kLog2e : 0.f;
+        hf[c][s] = live && a.state0 && (!LOCAL || seg == 0) ? a.state0[(chan + c) * N + n0 + s] : 0.f;
+      }
+    }
+    if (!LOCAL && seg > 0) {
+      // join the segments before this one: what each adds from a zero state,
+      // and its decay exp(A sum e); segment 0's holds the initial state
+      for (int q = 0; q < seg; ++q)
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) {
+          if (c_blk + c0 + c >= a.d) continue;
+          const float es = esum[q * per + chan + c];
+          float l[SPL];
+          lds<SPL>(l, hloc + (q * per + chan + c) * NP + n0);
+#pragma unroll
+          for (int s = 0; s < SPL; ++s) hf[c][s] = q == 0 ? l[s] : fmaf(ex2(Af[c][s] * es), hf[c][s], l[s]);
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < C2; ++c)
+#pragma unroll
+      for (int s = 0; s < SPL; ++s) {
+        A2[c][s] = pair(Af[2 * c][s], Af[2 * c + 1][s]);
+        hs[c][s] = pair(hf[2 * c][s], hf[2 * c + 1][s]);
+      }
+  }
+  float etot[CPL];
+#pragma unroll
+  for (int c = 0; c < CPL; ++c) etot[c] = 0.f;
+  const int mine = LaneSum<CPL, NL>::first(nl);
 
   __syncthreads();                                       // s_bias, s_D
-  for (long long t0 = t_seg; t0 < t_end; t0 += TQ) {
-    for (int i = tid; i < TQ * NP; i += nthr) {
-      const int t = i / NP, n = i % NP;
-      const bool live = t0 + t < t_end && n < N;
-      s_B[i] = live ? to_f(Bp[(t0 + t) * a.sB.t + n]) : 0.f;
-      if (!LOCAL) s_C[i] = live ? to_f(Cp[(t0 + t) * a.sC.t + n]) : 0.f;
+  int buf = 0;
+  for (long long t0 = t_seg; t0 < t_end; t0 += TQ, buf ^= 1) {
+    const T *raw = s_raw + buf * 3 * TQ * CB;
+    copies_done();
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+      const int i = tid + k * nthr;
+      if (i < TQ * NP) {
+        reinterpret_cast<float2 *>(s_B)[i] = make_float2(to_f(Br[k]), to_f(Br[k]));
+        if (!LOCAL) reinterpret_cast<float2 *>(s_C)[i] = make_float2(to_f(Cr[k]), to_f(Cr[k]));
+      }
     }
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int t = row_at(k), kc = col_at(k);
+      const int t = row_at(k), kc = col_at(k), at = t * CB + kc;
       const bool live = c_blk + kc < a.d && t0 + t < t_end;
+      const Vec<T, V> x = load_if<T, V>(raw + at, true), dt = load_if<T, V>(raw + TQ * CB + at, true);
+      float e[V], u[V];
+      lds<V>(e, s_bias + kc);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        float e = get(dr[k], i) + s_bias[kc + i];
-        if (a.softplus) e = softplus(e);
-        e = live ? e : 0.f;                              // a row behind the end leaves the state alone
-        s_e[t * CB + kc + i] = e;
-        s_u[t * CB + kc + i] = e * get(xr[k], i);
+        e[i] += get(dt, i);
+        if (a.softplus) e[i] = softplus(e[i]);
+        e[i] = live ? e[i] : 0.f;                        // a row behind the end leaves the state alone
+        u[i] = e[i] * get(x, i);
       }
-      xk[k] = xr[k];
-      if (!LOCAL) zk[k] = zr[k];
+      sts<V>(s_e + at, e);
+      sts<V>(s_u + at, u);
     }
     __syncthreads();
-    fetch(t0 + TQ);
+    fetch(t0 + TQ, buf ^ 1);
 
+    if (!idle)
 #pragma unroll 4
     for (int t = 0; t < TQ; ++t) {
-      float e[CPL], u[CPL], B[SPL], C[SPL], y[CPL];
+      float e[CPL], u[CPL], B[2 * SPL], C[2 * SPL];
       lds<CPL>(e, s_e + t * CB + c0);
       lds<CPL>(u, s_u + t * CB + c0);
-      lds<SPL>(B, s_B + t * NP + n0);
-      if (!LOCAL) lds<SPL>(C, s_C + t * NP + n0);
+      lds<2 * SPL>(B, s_B + (t * NP + n0) * 2);
+      if (!LOCAL) lds<2 * SPL>(C, s_C + (t * NP + n0) * 2);
+      F2 y[C2];
 #pragma unroll
-      for (int c = 0; c < CPL; ++c) y[c] = 0.f;
-#pragma unroll
-      for (int c = 0; c < CPL; ++c) {
-        if (LOCAL) ehold[c] += e[c];
+      for (int c = 0; c < C2; ++c) {
+        const F2 ee = pair(e[2 * c], e[2 * c + 1]), uu = pair(u[2 * c], u[2 * c + 1]);
+        if (LOCAL) {
+          etot[2 * c] += e[2 * c];
+          etot[2 * c + 1] += e[2 * c + 1];
+        }
 #pragma unroll
         for (int s = 0; s < SPL; ++s) {
-          hs[c][s] = fmaf(ex2(e[c] * A2[c][s]), hs[c][s], u[c] * B[s]);
-          if (!LOCAL) y[c] = fmaf(C[s], hs[c][s], y[c]);
+          hs[c][s] = fma(ex2(mul(ee, A2[c][s])), hs[c][s], mul(uu, pair(B[2 * s], B[2 * s + 1])));
+          if (!LOCAL) {
+            const F2 CC = pair(C[2 * s], C[2 * s + 1]);
+            y[c] = s ? fma(CC, hs[c][s], y[c]) : mul(CC, hs[c][s]);
+          }
         }
       }
       if (!LOCAL) {
-        LaneSum<CPL, NL>::run(y, nl);
+        float yv[CPL];
+#pragma unroll
+        for (int c = 0; c < C2; ++c) unpair(yv[2 * c], yv[2 * c + 1], y[c]);
+        LaneSum<CPL, NL>::run(yv, nl);
         // the channels' u of this token have been read by every lane of the warp
         if (nl < LaneSum<CPL, NL>::writers) {
 #pragma unroll
-          for (int i = 0; i < LaneSum<CPL, NL>::kept; ++i) s_u[t * CB + c0 + rotate + i] = y[i];
+          for (int i = 0; i < LaneSum<CPL, NL>::kept; ++i) s_u[t * CB + c0 + mine + i] = yv[i];
         }
       }
     }
@@ -177,48 +232,58 @@ __global__ void __launch_bounds__(128, V > 1 ? 4 : 2) scan_kernel(const Scan a, 
       // the next tile's staging needs no barrier after this
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
-        const int t = row_at(k), kc = col_at(k);
+        const int t = row_at(k), kc = col_at(k), at = t * CB + kc;
+        const Vec<T, V> x = load_if<T, V>(raw + at, true), z = load_if<T, V>(raw + 2 * TQ * CB + at, zp != nullptr);
+        float y[V], D[V];
+        lds<V>(y, s_u + at);
+        lds<V>(D, s_D + kc);
         Row<V> o;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          float y = fmaf(s_D[kc + i], get(xk[k], i), s_u[t * CB + kc + i]);
-          if (zp) y *= silu(get(zk[k], i));
-          put(o, i, y);
+          y[i] = fmaf(D[i], get(x, i), y[i]);
+          if (zp) y[i] *= silu(get(z, i));
+          put(o, i, y[i]);
         }
         if (c_blk + kc < a.d && t0 + t < t_end) store(yp + (t0 + t) * a.sy.t + kc, o);
       }
     }
   }
+  copies_done();
 
-  if (LOCAL) {
 #pragma unroll
-    for (int c = 0; c < CPL; ++c) {
-      if (c_blk + c0 + c >= a.d) continue;
-      const long long at = seg * per + chan + c;
-      if (nl == 0) esum[at] = ehold[c];
-      *reinterpret_cast<float4 *>(hloc + at * NP + n0) = make_float4(hs[c][0], hs[c][1], hs[c][2], hs[c][3]);
+  for (int c = 0; c < CPL; ++c) {
+    if (c_blk + c0 + c >= a.d) continue;
+    float hf[SPL];
+#pragma unroll
+    for (int s = 0; s < SPL; ++s) {
+      float lo, hi;
+      unpair(lo, hi, hs[c / 2][s]);
+      hf[s] = c % 2 ? hi : lo;
     }
-  } else if (seg == pl.S - 1 && a.state_end) {
-#pragma unroll
-    for (int c = 0; c < CPL; ++c)
+    if (LOCAL) {
+      const long long at = seg * per + chan + c;
+      if (nl == 0) esum[at] = etot[c];
+      sts<SPL>(hloc + at * NP + n0, hf);
+    } else if (seg == pl.S - 1 && a.state_end) {
 #pragma unroll
       for (int s = 0; s < SPL; ++s)
-        if (c_blk + c0 + c < a.d && n0 + s < N) a.state_end[(chan + c) * N + n0 + s] = hs[c][s];
+        if (n0 + s < N) a.state_end[(chan + c) * N + n0 + s] = hf[s];
+    }
   }
 }
 
 // Segments: with few channels the sequence is split so that every scheduler
-// has a warp or two; the states at the segments' starts then take a pass of their own.
+// has four warps; the states at the segments' starts then take a pass of their
+// own, about two thirds of the main one, so a split of less than three is not worth it.
 template <int NL, int CPL>
 Plan plan_of(int B, int H, int T, int d) {
   constexpr int CW = 32 / NL * CPL;
   Plan p;
-  p.warps = 4;
-  while (p.warps > 1 && CW * p.warps / 2 >= d) p.warps /= 2;
+  p.warps = d <= 2 * CW ? 2 : 4;
   p.blocks = (d + CW * p.warps - 1) / (CW * p.warps);
-  const long long warps = (long long)B * H * p.blocks * p.warps;
-  const long long want = (long long)kSMs * 4 * 2;
-  long long S = warps * 2 > want ? 1 : want / warps;
+  const long long warps = (long long)B * H * ((d + CW - 1) / CW);
+  const long long want = (long long)kSMs * (getenv("TMW") ? atoi(getenv("TMW")) : 16);
+  long long S = want / warps;
   const long long most = T / 64;                   // at least 64 tokens a segment
   if (S > most) S = most;
   if (S < 3) S = 1;
@@ -227,23 +292,33 @@ Plan plan_of(int B, int H, int T, int d) {
   return p;
 }
 
-template <typename T, int NL, int CPL, int V>
-cudaError_t run(const Scan &c, cudaStream_t st) {
-  constexpr int CW = 32 / NL * CPL, TQ = tile_of(NL, V);
-  const Plan p = plan_of<NL, CPL>(c.B, c.H, c.T, c.d);
-  const int CB = CW * p.warps;
-  const size_t smem = (size_t)(2 * TQ * CB + 2 * TQ * NL * SPL + 2 * CB) * 4;
+template <typename T, int NL, int CPL, int V, int W>
+cudaError_t run(const Scan &c, const Plan &p, cudaStream_t st) {
+  constexpr size_t smem = Smem<T, NL, CPL, V, W>::bytes;
+  auto local = scan_kernel<T, NL, CPL, V, W, true>;
+  auto whole = scan_kernel<T, NL, CPL, V, W, false>;
   const long long units = (long long)c.B * c.H * p.blocks;
   if (units * p.S > 0x7fffffffLL) return cudaErrorInvalidValue;
+  if (smem > 48 * 1024)
+    for (auto kern : {local, whole}) {
+      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (e != cudaSuccess) return e;
+    }
   float *hloc = static_cast<float *>(c.ws);
   float *esum = hloc + (size_t)(p.S - 1) * c.B * c.H * c.d * NL * SPL;
   if (p.S > 1) {
-    scan_kernel<T, NL, CPL, V, true><<<(unsigned)(units * (p.S - 1)), 32 * p.warps, smem, st>>>(c, p, hloc, esum);
+    local<<<(unsigned)(units * (p.S - 1)), 32 * W, smem, st>>>(c, p, hloc, esum);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  scan_kernel<T, NL, CPL, V, false><<<(unsigned)(units * p.S), 32 * p.warps, smem, st>>>(c, p, hloc, esum);
+  whole<<<(unsigned)(units * p.S), 32 * W, smem, st>>>(c, p, hloc, esum);
   return cudaGetLastError();
+}
+
+template <typename T, int NL, int V>
+cudaError_t plan_and_run(const Scan &c, cudaStream_t st) {
+  const Plan p = plan_of<NL, 4>(c.B, c.H, c.T, c.d);
+  return p.warps == 2 ? run<T, NL, 4, V, 2>(c, p, st) : run<T, NL, 4, V, 4>(c, p, st);
 }
 
 template <typename T>
@@ -255,11 +330,11 @@ cudaError_t dispatch(const Scan &c, cudaStream_t st) {
            fits(c.y, c.sy, c.d, V, el);
   };
   switch (lanes_of(c.N)) {
-    case 2: return vec(W16) ? run<T, 2, 4, W16>(c, st) : run<T, 2, 4, 1>(c, st);
-    case 4: return vec(W16) ? run<T, 4, 4, W16>(c, st) : run<T, 4, 4, 1>(c, st);
-    case 8: return vec(W16) ? run<T, 8, 4, W16>(c, st) : run<T, 8, 4, 1>(c, st);
-    case 16: return vec(4) ? run<T, 16, 4, 4>(c, st) : run<T, 16, 4, 1>(c, st);
-    default: return vec(2) ? run<T, 32, 4, 2>(c, st) : run<T, 32, 4, 1>(c, st);
+    case 2: return vec(W16) ? plan_and_run<T, 2, W16>(c, st) : plan_and_run<T, 2, 1>(c, st);
+    case 4: return vec(W16) ? plan_and_run<T, 4, W16>(c, st) : plan_and_run<T, 4, 1>(c, st);
+    case 8: return vec(W16) ? plan_and_run<T, 8, W16>(c, st) : plan_and_run<T, 8, 1>(c, st);
+    case 16: return vec(4) ? plan_and_run<T, 16, 4>(c, st) : plan_and_run<T, 16, 1>(c, st);
+    default: return vec(2) ? plan_and_run<T, 32, 2>(c, st) : plan_and_run<T, 32, 1>(c, st);
   }
 }
 

@@ -59,14 +59,6 @@ struct LaneSum {
   }
 };
 
-// M consecutive floats of shared memory as one load
-template <int M>
-__device__ __forceinline__ void lds(float (&v)[M], const float *p) {
-  const Vec<float, M> q = *reinterpret_cast<const Vec<float, M> *>(p);
-#pragma unroll
-  for (int i = 0; i < M; ++i) v[i] = q.e[i];
-}
-
 // Lanes that share a channel for N states.
 inline int lanes_of(int N) {
   int nl = 2;

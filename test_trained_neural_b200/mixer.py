@@ -15,17 +15,24 @@ made here (a given output keeps what it held there).
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
+import struct
 
 import torch
 
 from . import _native as N
 
-_TYPES = {torch.float32: N.TM_F32, torch.bfloat16: N.TM_BF16}
+_F32, _BF16, _I32 = torch.float32, torch.bfloat16, torch.int32
+_TYPES = {_F32: N.TM_F32, _BF16: N.TM_BF16}
 _ACTS = {"silu": N.TM_ACT_SILU, "none": N.TM_ACT_NONE, None: N.TM_ACT_NONE}
 _OVER = {"token": N.TM_NORM_TOKEN, "sequence": N.TM_NORM_SEQUENCE}
 
+
+# A decode step is a few microseconds on the GPU, and its call should not take
+# longer on the host: each entry point tests its tensors in one expression and
+# only asks _check for the reason when that fails; tables of strides are packed
+# bytes; workspace sizes are remembered by the problem's sizes.
 
 def _dtype_code(name, t):
     code = _TYPES.get(t.dtype)
@@ -41,8 +48,9 @@ def _named(table, name, value):
 
 
 def _check(device, **tensors):
-    """name=(tensor or None, shape, dtype): the right shape, type and device,
-    contiguous in the last dimension (token tensors) or altogether."""
+    """name=(tensor or None, shape, dtype, strided): raises for the first that has
+    another shape, type or device, or that is not contiguous (its channels, if
+    `strided`)."""
     for name, (t, shape, dtype, strided) in tensors.items():
         if t is None:
             continue
@@ -60,61 +68,72 @@ def _check(device, **tensors):
             raise ValueError(f"the channels of {name} must be contiguous")
 
 
-def _rank(name, t, n):
-    if t.dim() != n or t.numel() == 0:
-        raise ValueError(f"{name} must be a non-empty tensor of {n} dimensions, got shape {tuple(t.shape)}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
+def _par(t, shape, dev):
+    """A float32 parameter or state as the library wants it (or absent)."""
+    return t is None or (t.dtype is _F32 and t.get_device() == dev and t.shape == shape and t.is_contiguous())
+
+
+def _tok(t, shape, kind, dev):
+    """A token tensor (strides are looked at by _strides), or absent."""
+    return t is None or (t.dtype is kind and t.get_device() == dev and t.shape == shape)
+
+
+def _shape(name, t, n):
+    shape = t.shape
+    if len(shape) != n or 0 in shape:
+        raise ValueError(f"{name} must be a non-empty tensor of {n} dimensions, got shape {tuple(shape)}")
+    return shape
 
 
 def _p(t):
     return None if t is None else t.data_ptr()
 
 
-def _strides(*tensors):
-    """The library's table of (batch, head, token) strides; None when every
-    tensor is contiguous. Tensors of single tokens have no token stride."""
-    if all(t is None or t.is_contiguous() for t in tensors):
-        return None
-    table = []
-    for t in tensors:
+_PACK = {n: struct.Struct(f"{3 * n}q").pack for n in range(1, 10)}
+
+
+def _strides(names, *tensors):
+    """The library's table of (batch, head, token) strides; None when every tensor
+    is contiguous. Tensors of single tokens have no token stride."""
+    table, plain = [], True
+    for i, t in enumerate(tensors):
         if t is None:
             table += (0, 0, 0)
-        else:
-            s = t.stride()
-            table += (s[0], s[1], s[2] if len(s) == 4 else 0)
-    return (ctypes.c_longlong * len(table))(*table)
+            continue
+        s = t.stride()
+        if s[-1] != 1 and t.shape[-1] > 1:
+            raise ValueError(f"the channels of {names.split()[i]} must be contiguous")
+        if plain and not t.is_contiguous():
+            plain = False
+        table += s[:3] if len(s) == 4 else (s[0], s[1], 0)
+    return None if plain else _PACK[len(tensors)](*table)
 
 
-@contextlib.contextmanager
-def _on_stream(device, stream, used):
-    """Makes `stream` current, so that what is allocated belongs to it, and tells
-    the allocator that it uses the caller's tensors."""
-    with torch.cuda.device(device), torch.cuda.stream(stream):
-        for t in used:
-            if t is not None:
-                t.record_stream(stream)
-        yield
-
-
-def _placed(fn):
-    """Runs fn on its tensors' device and on the given stream."""
-    def call(x, *args, stream=None, **kwargs):
-        if not isinstance(x, torch.Tensor) or not x.is_cuda:
-            raise ValueError("x must be a CUDA tensor")
-        index = x.device.index
+def _elsewhere(fn, stream, x, args, kwargs):
+    """fn on another device than the current one, or on a given stream: with both
+    made current, so that what fn allocates belongs to them, and the allocator
+    told that the stream uses the caller's tensors."""
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    with torch.cuda.device(x.device):
         if stream is None:
-            if index == torch.cuda.current_device():
-                return fn(x, *args, _stream=torch.cuda.current_stream(index).cuda_stream, **kwargs)
-            with torch.cuda.device(index):
-                return fn(x, *args, _stream=torch.cuda.current_stream(index).cuda_stream, **kwargs)
-        if stream.device.index != index:
+            return fn(x, *args, **kwargs)
+        if stream.device != x.device:
             raise ValueError(f"stream is on {stream.device}, x on {x.device}")
-        used = [t for t in (x, *args, *kwargs.values()) if isinstance(t, torch.Tensor)]
-        with _on_stream(x.device, stream, used):
-            return fn(x, *args, _stream=stream.cuda_stream, **kwargs)
-    call.__name__, call.__doc__, call.__wrapped__ = fn.__name__, fn.__doc__, fn
-    return call
+        with torch.cuda.stream(stream):
+            for t in (x, *args, *kwargs.values()):
+                if isinstance(t, torch.Tensor) and t.is_cuda:
+                    t.record_stream(stream)
+            return fn(x, *args, **kwargs)
+
+
+def _here(x, stream):
+    """Whether x's device is the current one and the call goes to its current stream."""
+    return stream is None and x.is_cuda and x.get_device() == torch.cuda.current_device()
+
+
+def _stream_of(dev):
+    return torch.cuda.current_stream(dev).cuda_stream
 
 
 def _fresh(like, lengths, dtype=None):
@@ -122,58 +141,66 @@ def _fresh(like, lengths, dtype=None):
     return torch.empty_like(like, dtype=dtype) if lengths is None else torch.zeros_like(like, dtype=dtype)
 
 
-def _workspace(given, size_fn, *args, device):
+@functools.lru_cache(maxsize=4096)
+def _workspace_size(fn, *sizes):
     n = ctypes.c_size_t()
-    N.check(getattr(N.load(), size_fn)(*args, ctypes.byref(n)), size_fn)
+    N.check(getattr(N.load(), fn)(*sizes, ctypes.byref(n)), fn)
+    return n.value
+
+
+def _workspace(given, x, fn, *sizes):
+    """(tensor or None, bytes)"""
     if given is None:
-        return (None, 0) if n.value == 0 else _pair(torch.empty(n.value, dtype=torch.uint8, device=device))
-    if given.dtype != torch.uint8 or not given.is_contiguous() or given.device != device:
-        raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
-    return _pair(given)
+        n = _workspace_size(fn, *sizes)
+        return (x.new_empty(n, dtype=torch.uint8) if n else None), n
+    if given.dtype != torch.uint8 or not given.is_contiguous() or given.device != x.device:
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {x.device}")
+    return given, given.numel()
 
 
-def _pair(ws):
-    return ws, ws.numel()
+def _conv_check(x, shape, filt, bias, hist, lengths, more):
+    w, dev, kind = filt.shape[-1], x.device, x.dtype
+    H, d = shape[1], shape[-1]
+    _check(dev, filt=(filt, (H, d, w), _F32, False), bias=(bias, (H, d), _F32, False),
+           hist=(hist, (shape[0], H, w - 1, d), kind, False), lengths=(lengths, (shape[0],), _I32, False), **more)
 
 
-@_placed
-def short_conv(x, filt, bias=None, *, hist=None, lengths=None, act="silu", out=None, tail=None, _stream=None):
+def short_conv(x, filt, bias=None, *, hist=None, lengths=None, act="silu", out=None, tail=None, stream=None):
     """Depthwise causal convolution act(bias + sum_j filt[..., j] x[t - j]).
 
     x [B, H, T, d]; filt [H, d, width] (width <= 8) and bias [H, d] float32; hist
     [B, H, width-1, d], the tokens before the call. Returns (y, tail): tail, like
     hist, holds the last width-1 tokens, the history of the next call."""
-    _rank("x", x, 4)
-    B, H, T, d = x.shape
-    w, dev, dt = filt.shape[-1], x.device, x.dtype
-    code = _dtype_code("x", x)
-    _check(dev, x=(x, (B, H, T, d), dt, True), filt=(filt, (H, d, w), torch.float32, False),
-           bias=(bias, (H, d), torch.float32, False), hist=(hist, (B, H, w - 1, d), dt, False),
-           lengths=(lengths, (B,), torch.int32, False), out=(out, (B, H, T, d), dt, True),
-           tail=(tail, (B, H, w - 1, d), dt, False))
+    if not _here(x, stream):
+        return _elsewhere(short_conv, stream, x, (filt, bias),
+                          dict(hist=hist, lengths=lengths, act=act, out=out, tail=tail))
+    shape = B, H, T, d = _shape("x", x, 4)
+    w, kind = filt.shape[-1], x.dtype
+    code, past = _dtype_code("x", x), (B, H, w - 1, d)
+    _conv_check(x, shape, filt, bias, hist, lengths, {"out": (out, shape, kind, True), "tail": (tail, past, kind, False)})
     if out is None:
         out = _fresh(x, lengths)
     if tail is None:
-        tail = torch.empty((B, H, w - 1, d), dtype=dt, device=dev)
-    N.check(N.load().tm_conv(B, H, T, d, w, code, _named(_ACTS, "act", act), _p(x), _p(filt), _p(bias), _p(hist),
-                             _p(lengths), _p(out), _p(tail), _strides(x, out), _stream), "tm_conv")
+        tail = x.new_empty(past)
+    N.check(N.load().tm_conv(B, H, T, d, w, code, _named(_ACTS, "act", act), x.data_ptr(), filt.data_ptr(), _p(bias),
+                             _p(hist), _p(lengths), out.data_ptr(), tail.data_ptr(), _strides("x out", x, out),
+                             _stream_of(x.get_device())), "tm_conv")
     return out, tail
 
 
-@_placed
 def short_conv_backward(x, filt, dy, bias=None, *, hist=None, lengths=None, act="silu", dtail=None, workspace=None,
-                        _stream=None):
+                        stream=None):
     """Gradients of sum <dy, y> + <dtail, tail> for short_conv of these inputs:
     a dict of dx, dfilt, dbias (with a bias) and dhist (with a history)."""
-    _rank("x", x, 4)
-    B, H, T, d = x.shape
-    w, dev, dt = filt.shape[-1], x.device, x.dtype
+    if not _here(x, stream):
+        return _elsewhere(short_conv_backward, stream, x, (filt, dy, bias),
+                          dict(hist=hist, lengths=lengths, act=act, dtail=dtail, workspace=workspace))
+    shape = B, H, T, d = _shape("x", x, 4)
+    w, kind = filt.shape[-1], x.dtype
     code = _dtype_code("x", x)
-    _check(dev, x=(x, (B, H, T, d), dt, True), filt=(filt, (H, d, w), torch.float32, False),
-           dy=(dy, (B, H, T, d), dt, True), bias=(bias, (H, d), torch.float32, False),
-           hist=(hist, (B, H, w - 1, d), dt, False), lengths=(lengths, (B,), torch.int32, False),
-           dtail=(dtail, (B, H, w - 1, d), dt, False))
-    ws, n = _workspace(workspace, "tm_conv_backward_workspace_size", B, H, T, d, w, code, device=dev)
+    _conv_check(x, shape, filt, bias, hist, lengths, {"dy": (dy, shape, kind, True),
+                                                      "dtail": (dtail, (B, H, w - 1, d), kind, False)})
+    ws, n = _workspace(workspace, x, "tm_conv_backward_workspace_size", B, H, T, d, w, code)
     out = {"dx": torch.empty_like(x), "dfilt": torch.empty_like(filt)}
     if bias is not None:
         out["dbias"] = torch.empty_like(bias)
@@ -182,30 +209,33 @@ def short_conv_backward(x, filt, dy, bias=None, *, hist=None, lengths=None, act=
     N.check(N.load().tm_conv_backward(
         B, H, T, d, w, code, _named(_ACTS, "act", act), _p(x), _p(filt), _p(bias), _p(hist), _p(lengths), _p(dy),
         _p(dtail), _p(out["dx"]), _p(out["dfilt"]), _p(out.get("dbias")), _p(out.get("dhist")),
-        _strides(x, dy, out["dx"]), _p(ws), n, _stream), "tm_conv_backward")
+        _strides("x dy dx", x, dy, out["dx"]), _p(ws), n, _stream_of(x.get_device())), "tm_conv_backward")
     return out
 
 
-@_placed
-def short_conv_step(x, hist, filt, bias=None, *, act="silu", out=None, _stream=None):
+def short_conv_step(x, hist, filt, bias=None, *, act="silu", out=None, stream=None):
     """short_conv of one token per sequence, x [B, H, d]: returns y and moves
     hist [B, H, width-1, d] on in place."""
-    _rank("x", x, 3)
-    B, H, d = x.shape
-    w, dev, dt = filt.shape[-1], x.device, x.dtype
+    if not _here(x, stream):
+        return _elsewhere(short_conv_step, stream, x, (hist, filt, bias), dict(act=act, out=out))
+    shape = B, H, d = _shape("x", x, 3)
+    w, kind, dev = filt.shape[-1], x.dtype, x.get_device()
     code = _dtype_code("x", x)
-    _check(dev, x=(x, (B, H, d), dt, True), hist=(hist, (B, H, w - 1, d), dt, False),
-           filt=(filt, (H, d, w), torch.float32, False), bias=(bias, (H, d), torch.float32, False),
-           out=(out, (B, H, d), dt, True))
+    past = (B, H, w - 1, d)
+    if not (_par(filt, (H, d, w), dev) and _par(bias, (H, d), dev) and _tok(hist, past, kind, dev) and
+            hist.is_contiguous() and _tok(out, shape, kind, dev)):
+        _conv_check(x, shape, filt, bias, hist, None, {"out": (out, shape, kind, True)})
     if out is None:
-        out = torch.empty((B, H, d), dtype=dt, device=dev)
-    N.check(N.load().tm_conv_step(B, H, d, w, code, _named(_ACTS, "act", act), _p(x), _p(filt), _p(bias), _p(hist),
-                                  _p(out), _strides(x, out), _stream), "tm_conv_step")
+        out = x.new_empty(shape)
+    N.check(N.load().tm_conv_step(B, H, d, w, code, _named(_ACTS, "act", act), x.data_ptr(), filt.data_ptr(), _p(bias),
+                                  hist.data_ptr(), out.data_ptr(), _strides("x out", x, out), _stream_of(dev)),
+            "tm_conv_step")
     return out
 
 
-def _scan_check(x, dt, A, Bm, Cm, D, z, dt_bias, state, more):
-    shape, dev, kind, f32 = x.shape, x.device, x.dtype, torch.float32
+def _scan_sizes(x, shape, dt, A, Bm, Cm, D, z, dt_bias, state, state2, token2, lengths):
+    """Checks what the three scan calls share; (G, N)."""
+    kind, dev = x.dtype, x.get_device()
     B, H, d = shape[0], shape[1], shape[-1]
     if Bm.dim() != len(shape) or A.dim() != 3:
         raise ValueError(f"A must be [H, d, N] and Bm [B, G, {'T, ' if len(shape) == 4 else ''}N], got "
@@ -213,142 +243,151 @@ def _scan_check(x, dt, A, Bm, Cm, D, z, dt_bias, state, more):
     G, n = Bm.shape[1], A.shape[-1]
     if G == 0 or H % G:
         raise ValueError(f"the {G} groups of Bm must divide the {H} heads")
-    group = (B, G, *shape[2:-1], n)
-    _check(dev, x=(x, shape, kind, True), dt=(dt, shape, kind, True), A=(A, (H, d, n), f32, False),
-           Bm=(Bm, group, kind, True), Cm=(Cm, group, kind, True), D=(D, (H, d), f32, False),
-           z=(z, shape, kind, True), dt_bias=(dt_bias, (H, d), f32, False), state=(state, (B, H, d, n), f32, False),
-           **more)
+    group = (B, G, shape[2], n) if len(shape) == 4 else (B, G, n)
+    par, held = (H, d), (B, H, d, n)
+    if not (_tok(dt, shape, kind, dev) and _tok(z, shape, kind, dev) and _tok(token2, shape, kind, dev) and
+            _tok(Bm, group, kind, dev) and _tok(Cm, group, kind, dev) and _par(A, (H, d, n), dev) and
+            _par(D, par, dev) and _par(dt_bias, par, dev) and _par(state, held, dev) and _par(state2, held, dev) and
+            lengths is None):
+        _check(x.device, dt=(dt, shape, kind, True), A=(A, (H, d, n), _F32, False), Bm=(Bm, group, kind, True),
+               Cm=(Cm, group, kind, True), D=(D, par, _F32, False), z=(z, shape, kind, True),
+               dt_bias=(dt_bias, par, _F32, False), state=(state, held, _F32, False),
+               lengths=(lengths, (B,), _I32, False), **{"out or dy": (token2, shape, kind, True),
+                                                       "state_end or its gradient": (state2, held, _F32, False)})
     return G, n
 
 
-@_placed
 def selective_scan(x, dt, A, Bm, Cm, *, D=None, z=None, dt_bias=None, state=None, lengths=None, softplus=True,
-                   out=None, state_end=None, workspace=None, _stream=None):
+                   out=None, state_end=None, workspace=None, stream=None):
     """Selective state-space scan: h = exp(e A) h + e x Bm, y = (Cm h + D x) silu(z),
     e = softplus(dt + dt_bias).
 
     x, dt, z [B, H, T, d]; Bm, Cm [B, G, T, N] (G divides H); A [H, d, N], D and
     dt_bias [H, d], state [B, H, d, N] float32. Returns (y, state_end); pass
     state_end=state to update in place."""
-    _rank("x", x, 4)
-    B, H, T, d = x.shape
+    if not _here(x, stream):
+        return _elsewhere(selective_scan, stream, x, (dt, A, Bm, Cm),
+                          dict(D=D, z=z, dt_bias=dt_bias, state=state, lengths=lengths, softplus=softplus, out=out,
+                               state_end=state_end, workspace=workspace))
+    shape = B, H, T, d = _shape("x", x, 4)
     code = _dtype_code("x", x)
-    G, n = _scan_check(x, dt, A, Bm, Cm, D, z, dt_bias, state, {"lengths": (lengths, (B,), torch.int32, False),
-                                                               "out": (out, x.shape, x.dtype, True)})
-    _check(x.device, state_end=(state_end, (B, H, d, n), torch.float32, False))
+    G, n = _scan_sizes(x, shape, dt, A, Bm, Cm, D, z, dt_bias, state, state_end, out, lengths)
     if out is None:
         out = _fresh(x, lengths)
     if state_end is None:
-        state_end = torch.empty((B, H, d, n), dtype=torch.float32, device=x.device)
-    ws, nb = _workspace(workspace, "tm_scan_workspace_size", B, H, G, T, d, n, code, device=x.device)
-    N.check(N.load().tm_scan(B, H, G, T, d, n, code, int(softplus), _p(x), _p(dt), _p(A), _p(Bm), _p(Cm), _p(D), _p(z),
-                             _p(dt_bias), _p(state), _p(lengths), _p(out), _p(state_end),
-                             _strides(x, dt, Bm, Cm, z, out), _p(ws), nb, _stream), "tm_scan")
+        state_end = A.new_empty((B, H, d, n))
+    ws, nb = _workspace(workspace, x, "tm_scan_workspace_size", B, H, G, T, d, n, code)
+    N.check(N.load().tm_scan(B, H, G, T, d, n, code, bool(softplus), x.data_ptr(), dt.data_ptr(), A.data_ptr(),
+                             Bm.data_ptr(), Cm.data_ptr(), _p(D), _p(z), _p(dt_bias), _p(state), _p(lengths),
+                             out.data_ptr(), state_end.data_ptr(),
+                             _strides("x dt Bm Cm z out", x, dt, Bm, Cm, z, out), _p(ws), nb,
+                             _stream_of(x.get_device())), "tm_scan")
     return out, state_end
 
 
-@_placed
 def selective_scan_backward(x, dt, A, Bm, Cm, dy, *, D=None, z=None, dt_bias=None, state=None, dstate_end=None,
-                            lengths=None, softplus=True, workspace=None, _stream=None):
+                            lengths=None, softplus=True, workspace=None, stream=None):
     """Gradients of sum <dy, y> + <dstate_end, state_end> for selective_scan of
     these inputs: a dict of dx, ddt, dA, dB, dC and, where the input is given,
     dD, dz, ddt_bias and dstate."""
-    _rank("x", x, 4)
-    B, H, T, d = x.shape
+    if not _here(x, stream):
+        return _elsewhere(selective_scan_backward, stream, x, (dt, A, Bm, Cm, dy),
+                          dict(D=D, z=z, dt_bias=dt_bias, state=state, dstate_end=dstate_end, lengths=lengths,
+                               softplus=softplus, workspace=workspace))
+    shape = B, H, T, d = _shape("x", x, 4)
     code = _dtype_code("x", x)
-    G, n = _scan_check(x, dt, A, Bm, Cm, D, z, dt_bias, state, {"lengths": (lengths, (B,), torch.int32, False),
-                                                               "dy": (dy, x.shape, x.dtype, True)})
-    _check(x.device, dstate_end=(dstate_end, (B, H, d, n), torch.float32, False))
-    ws, nb = _workspace(workspace, "tm_scan_backward_workspace_size", B, H, G, T, d, n, code, device=x.device)
-    group = dict(dtype=x.dtype, device=x.device)
+    G, n = _scan_sizes(x, shape, dt, A, Bm, Cm, D, z, dt_bias, state, dstate_end, dy, lengths)
+    ws, nb = _workspace(workspace, x, "tm_scan_backward_workspace_size", B, H, G, T, d, n, code)
     out = {"dx": torch.empty_like(x), "ddt": torch.empty_like(dt), "dA": torch.empty_like(A),
-           "dB": torch.empty((B, G, T, n), **group), "dC": torch.empty((B, G, T, n), **group)}
+           "dB": x.new_empty((B, G, T, n)), "dC": x.new_empty((B, G, T, n))}
     for name, t in (("dD", D), ("dz", z), ("ddt_bias", dt_bias), ("dstate", state)):
         if t is not None:
             out[name] = torch.empty_like(t)
     N.check(N.load().tm_scan_backward(
-        B, H, G, T, d, n, code, int(softplus), _p(x), _p(dt), _p(A), _p(Bm), _p(Cm), _p(D), _p(z), _p(dt_bias),
+        B, H, G, T, d, n, code, bool(softplus), _p(x), _p(dt), _p(A), _p(Bm), _p(Cm), _p(D), _p(z), _p(dt_bias),
         _p(state), _p(lengths), _p(dy), _p(dstate_end), _p(out["dx"]), _p(out["ddt"]), _p(out["dA"]), _p(out["dB"]),
         _p(out["dC"]), _p(out.get("dD")), _p(out.get("dz")), _p(out.get("ddt_bias")), _p(out.get("dstate")),
-        _strides(x, dt, Bm, Cm, z, dy, out["dx"], out["ddt"], out.get("dz")), _p(ws), nb, _stream), "tm_scan_backward")
+        _strides("x dt Bm Cm z dy dx ddt dz", x, dt, Bm, Cm, z, dy, out["dx"], out["ddt"], out.get("dz")), _p(ws), nb,
+        _stream_of(x.get_device())), "tm_scan_backward")
     return out
 
 
-@_placed
 def selective_scan_step(x, dt, A, Bm, Cm, state, *, D=None, z=None, dt_bias=None, softplus=True, out=None,
-                        _stream=None):
+                        stream=None):
     """selective_scan of one token per sequence, x, dt, z [B, H, d], Bm, Cm
     [B, G, N]: returns y and updates state [B, H, d, N] in place."""
-    _rank("x", x, 3)
-    B, H, d = x.shape
+    if not _here(x, stream):
+        return _elsewhere(selective_scan_step, stream, x, (dt, A, Bm, Cm, state),
+                          dict(D=D, z=z, dt_bias=dt_bias, softplus=softplus, out=out))
+    shape = B, H, d = _shape("x", x, 3)
     code = _dtype_code("x", x)
-    G, n = _scan_check(x, dt, A, Bm, Cm, D, z, dt_bias, state, {"out": (out, x.shape, x.dtype, True)})
+    G, n = _scan_sizes(x, shape, dt, A, Bm, Cm, D, z, dt_bias, state, None, out, None)
     if out is None:
-        out = torch.empty((B, H, d), dtype=x.dtype, device=x.device)
-    N.check(N.load().tm_scan_step(B, H, G, d, n, code, int(softplus), _p(x), _p(dt), _p(A), _p(Bm), _p(Cm), _p(D),
-                                  _p(z), _p(dt_bias), _p(state), _p(out), _strides(x, dt, Bm, Cm, z, out), _stream),
-            "tm_scan_step")
+        out = x.new_empty(shape)
+    N.check(N.load().tm_scan_step(B, H, G, d, n, code, bool(softplus), x.data_ptr(), dt.data_ptr(), A.data_ptr(),
+                                  Bm.data_ptr(), Cm.data_ptr(), _p(D), _p(z), _p(dt_bias), state.data_ptr(),
+                                  out.data_ptr(), _strides("x dt Bm Cm z out", x, dt, Bm, Cm, z, out),
+                                  _stream_of(x.get_device())), "tm_scan_step")
     return out
 
 
-def _norm_shapes(x, over):
-    B, H, T, d = x.shape
-    return (B, H, T, 2) if over == "token" else (B, H, 2)
+def _norm_check(x, shape, weight, bias, lengths, stats, over, more):
+    B, H, T, d = shape
+    kept = (B, H, T, 2) if over == "token" else (B, H, 2)
+    _check(x.device, weight=(weight, (H, d), _F32, False), bias=(bias, (H, d), _F32, False),
+           lengths=(lengths, (B,), _I32, False), stats=(stats, kept, _F32, False), **more)
+    return kept
 
 
-@_placed
 def group_norm(x, weight=None, bias=None, *, over="token", act=None, eps=1e-5, lengths=None, dtype=None, out=None,
-               stats=None, workspace=None, _stream=None):
+               stats=None, workspace=None, stream=None):
     """act(weight (x - mean) / sqrt(var + eps) + bias), the statistics of each
     head over the channels of one token (over="token") or of the whole sequence
     (over="sequence": group norm of a channels-last [B, T, H * d] tensor, passed as
     x.view(B, T, H, d).transpose(1, 2)). weight, bias [H, d] float32; `dtype`: the
     output's type (default: x's). Returns (y, stats) with stats = (mean, 1 /
     sqrt(var + eps)) [B, H, T, 2] or [B, H, 2] for group_norm_backward."""
-    _rank("x", x, 4)
-    B, H, T, d = x.shape
-    dev = x.device
+    if not _here(x, stream):
+        return _elsewhere(group_norm, stream, x, (weight, bias),
+                          dict(over=over, act=act, eps=eps, lengths=lengths, dtype=dtype, out=out, stats=stats,
+                               workspace=workspace))
+    shape = B, H, T, d = _shape("x", x, 4)
     kind = out.dtype if out is not None else dtype or x.dtype
     if dtype is not None and kind != dtype:
         raise TypeError(f"out must be {dtype}, got {kind}")
-    code, where = _dtype_code("x", x), _named(_OVER, "over", over)
     if kind not in _TYPES:
         raise TypeError(f"the output must be float32 or bfloat16, got {kind}")
-    _check(dev, x=(x, (B, H, T, d), x.dtype, True), weight=(weight, (H, d), torch.float32, False),
-           bias=(bias, (H, d), torch.float32, False), lengths=(lengths, (B,), torch.int32, False),
-           out=(out, (B, H, T, d), kind, True), stats=(stats, _norm_shapes(x, over), torch.float32, False))
+    code, where = _dtype_code("x", x), _named(_OVER, "over", over)
+    kept = _norm_check(x, shape, weight, bias, lengths, stats, over, {"out": (out, shape, kind, True)})
     if out is None:
         out = _fresh(x, lengths, kind)
     if stats is None:
-        make = torch.empty if lengths is None else torch.zeros
-        stats = make(_norm_shapes(x, over), dtype=torch.float32, device=dev)
-    ws, n = _workspace(workspace, "tm_group_norm_workspace_size", B, H, T, d, where, 0, device=dev)
-    N.check(N.load().tm_group_norm(B, H, T, d, where, code, _TYPES[kind], _named(_ACTS, "act", act), float(eps), _p(x),
-                                   _p(weight), _p(bias), _p(lengths), _p(out), _p(stats), _strides(x, out), _p(ws), n,
-                                   _stream), "tm_group_norm")
+        stats = (x.new_empty if lengths is None else x.new_zeros)(kept, dtype=_F32)
+    ws, n = _workspace(workspace, x, "tm_group_norm_workspace_size", B, H, T, d, where, 0)
+    N.check(N.load().tm_group_norm(B, H, T, d, where, code, _TYPES[kind], _named(_ACTS, "act", act), float(eps),
+                                   x.data_ptr(), _p(weight), _p(bias), _p(lengths), out.data_ptr(), stats.data_ptr(),
+                                   _strides("x out", x, out), _p(ws), n, _stream_of(x.get_device())), "tm_group_norm")
     return out, stats
 
 
-@_placed
 def group_norm_backward(x, dy, stats, weight=None, bias=None, *, over="token", act=None, lengths=None, workspace=None,
-                        _stream=None):
+                        stream=None):
     """Gradients of sum <dy, y> for group_norm of these inputs and the stats it
     returned: a dict of dx and, where the parameter is given, dweight and dbias."""
-    _rank("x", x, 4)
-    B, H, T, d = x.shape
-    dev = x.device
-    code, where = _dtype_code("x", x), _named(_OVER, "over", over)
-    _check(dev, x=(x, (B, H, T, d), x.dtype, True), dy=(dy, (B, H, T, d), dy.dtype, True),
-           weight=(weight, (H, d), torch.float32, False), bias=(bias, (H, d), torch.float32, False),
-           lengths=(lengths, (B,), torch.int32, False), stats=(stats, _norm_shapes(x, over), torch.float32, False))
-    ws, n = _workspace(workspace, "tm_group_norm_workspace_size", B, H, T, d, where, 1, device=dev)
+    if not _here(x, stream):
+        return _elsewhere(group_norm_backward, stream, x, (dy, stats, weight, bias),
+                          dict(over=over, act=act, lengths=lengths, workspace=workspace))
+    shape = B, H, T, d = _shape("x", x, 4)
+    code, where, out_code = _dtype_code("x", x), _named(_OVER, "over", over), _dtype_code("dy", dy)
+    _norm_check(x, shape, weight, bias, lengths, stats, over, {"dy": (dy, shape, dy.dtype, True)})
+    ws, n = _workspace(workspace, x, "tm_group_norm_workspace_size", B, H, T, d, where, 1)
     out = {"dx": torch.empty_like(x)}
     if weight is not None:
         out["dweight"] = torch.empty_like(weight)
     if bias is not None:
         out["dbias"] = torch.empty_like(bias)
     N.check(N.load().tm_group_norm_backward(
-        B, H, T, d, where, code, _dtype_code("dy", dy), _named(_ACTS, "act", act), _p(x), _p(dy), _p(stats), _p(weight),
-        _p(bias), _p(lengths), _p(out["dx"]), _p(out.get("dweight")), _p(out.get("dbias")), _strides(x, dy, out["dx"]),
-        _p(ws), n, _stream), "tm_group_norm_backward")
+        B, H, T, d, where, code, out_code, _named(_ACTS, "act", act), _p(x), _p(dy), _p(stats), _p(weight), _p(bias),
+        _p(lengths), _p(out["dx"]), _p(out.get("dweight")), _p(out.get("dbias")), _strides("x dy dx", x, dy, out["dx"]),
+        _p(ws), n, _stream_of(x.get_device())), "tm_group_norm_backward")
     return out
