@@ -25,24 +25,6 @@ __device__ __forceinline__ float rcp(float x) {
 __device__ __forceinline__ float sigmoid(float x) { return rcp(1.f + ex2(-kLog2e * x)); }
 __device__ __forceinline__ float silu(float x) { return x * sigmoid(x); }
 
-// log(1 + exp(v)) = max(v, 0) + log1p(u), u = exp(-|v|) in (0, 1]. log1p(u) / u
-// is smooth there: the polynomial through its 9 Chebyshev nodes on [0, 1] is
-// within 3.5e-8 of it (2e-7 as evaluated), so the result keeps fp32's relative
-// accuracy for every v (log(1 + u) itself would lose it for small u).
-__device__ __forceinline__ float softplus(float v) {
-  const float u = ex2(-kLog2e * fabsf(v));
-  float p = 5.126102144e-03f;
-  p = fmaf(p, u, -2.907406469e-02f);
-  p = fmaf(p, u, 7.751608676e-02f);
-  p = fmaf(p, u, -1.360224762e-01f);
-  p = fmaf(p, u, 1.907688074e-01f);
-  p = fmaf(p, u, -2.483539899e-01f);
-  p = fmaf(p, u, 3.331812171e-01f);
-  p = fmaf(p, u, -4.999944498e-01f);
-  p = fmaf(p, u, 9.999999659e-01f);
-  return v > -87.f ? fmaxf(v, 0.f) + u * p : ex2(kLog2e * v);
-}
-
 // V consecutive elements of one row as loaded: fp32 values, or bf16 pairs in
 // 32-bit words (a bf16 of its own would take a whole register).
 template <typename T, int V>
@@ -187,6 +169,63 @@ __device__ __forceinline__ F2 ex2(F2 x) {
   float a, b;
   unpair(a, b, x);
   return pair(ex2(a), ex2(b));
+}
+
+__device__ __forceinline__ F2 add(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 both(float a) { return pair(a, a); }
+__device__ __forceinline__ F2 rcp(F2 x) {
+  float a, b;
+  unpair(a, b, x);
+  return pair(rcp(a), rcp(b));
+}
+__device__ __forceinline__ F2 sigmoid(F2 x) { return rcp(add(both(1.f), ex2(mul(both(-kLog2e), x)))); }
+__device__ __forceinline__ F2 silu(F2 x) { return mul(x, sigmoid(x)); }
+
+// log(1 + exp(v)) = max(v, 0) + log1p(u), u = exp(-|v|) in (0, 1]. log1p(u) / u
+// is smooth there: the polynomial through its 9 Chebyshev nodes on [0, 1] is
+// within 3.5e-8 of it (2e-7 as evaluated), so the result keeps fp32's relative
+// accuracy for every v (log(1 + u) itself would lose it for small u).
+__device__ __forceinline__ F2 softplus(F2 v) {
+  float a, b;
+  unpair(a, b, v);
+  const F2 u = ex2(mul(both(-kLog2e), pair(fabsf(a), fabsf(b))));
+  F2 p = both(5.126102144e-03f);
+  p = fma(p, u, both(-2.907406469e-02f));
+  p = fma(p, u, both(7.751608676e-02f));
+  p = fma(p, u, both(-1.360224762e-01f));
+  p = fma(p, u, both(1.907688074e-01f));
+  p = fma(p, u, both(-2.483539899e-01f));
+  p = fma(p, u, both(3.331812171e-01f));
+  p = fma(p, u, both(-4.999944498e-01f));
+  p = fma(p, u, both(9.999999659e-01f));
+  return fma(u, p, pair(fmaxf(a, 0.f), fmaxf(b, 0.f)));
+}
+__device__ __forceinline__ float softplus(float v) {
+  float a, b;
+  unpair(a, b, softplus(both(v)));
+  return a;
+}
+
+// f of every value, two at a time
+template <int V, typename F>
+__device__ __forceinline__ void each(float (&v)[V], F f) {
+  if constexpr (V == 1) {
+    float b;
+    unpair(v[0], b, f(both(v[0])));
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) unpair(v[i], v[i + 1], f(pair(v[i], v[i + 1])));
+  }
+}
+template <typename T, int V>
+__device__ __forceinline__ void values(float (&v)[V], const T *p) {
+  const Vec<T, V> q = *reinterpret_cast<const Vec<T, V> *>(p);
+#pragma unroll
+  for (int i = 0; i < V; ++i) v[i] = get(q, i);
 }
 
 // Tokens of sequence b: the caller's length held to [0, T].

@@ -173,15 +173,17 @@ __global__ void __launch_bounds__(32 * W, (NL >= 16 ? 8 : 16) / W) scan_kernel(c
     for (int k = 0; k < NV; ++k) {
       const int t = row_at(k), kc = col_at(k), at = t * CB + kc;
       const bool live = c_blk + kc < a.d && t0 + t < t_end;
-      const Vec<T, V> x = load_if<T, V>(raw + at, true), dt = load_if<T, V>(raw + TQ * CB + at, true);
-      float e[V], u[V];
-      lds<V>(e, s_bias + kc);
+      float x[V], e[V], u[V], bias[V];
+      values<T, V>(x, raw + at);
+      values<T, V>(e, raw + TQ * CB + at);
+      lds<V>(bias, s_bias + kc);
+#pragma unroll
+      for (int i = 0; i < V; ++i) e[i] += bias[i];
+      if (a.softplus) each<V>(e, [](F2 v) { return softplus(v); });
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        e[i] += get(dt, i);
-        if (a.softplus) e[i] = softplus(e[i]);
         e[i] = live ? e[i] : 0.f;                        // a row behind the end leaves the state alone
-        u[i] = e[i] * get(x, i);
+        u[i] = e[i] * x[i];
       }
       sts<V>(s_e + at, e);
       sts<V>(s_u + at, u);
@@ -233,17 +235,22 @@ __global__ void __launch_bounds__(32 * W, (NL >= 16 ? 8 : 16) / W) scan_kernel(c
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
         const int t = row_at(k), kc = col_at(k), at = t * CB + kc;
-        const Vec<T, V> x = load_if<T, V>(raw + at, true), z = load_if<T, V>(raw + 2 * TQ * CB + at, zp != nullptr);
-        float y[V], D[V];
+        float x[V], y[V], D[V];
+        values<T, V>(x, raw + at);
         lds<V>(y, s_u + at);
         lds<V>(D, s_D + kc);
+#pragma unroll
+        for (int i = 0; i < V; ++i) y[i] = fmaf(D[i], x[i], y[i]);
+        if (zp) {
+          float z[V];
+          values<T, V>(z, raw + 2 * TQ * CB + at);
+          each<V>(z, [](F2 v) { return silu(v); });
+#pragma unroll
+          for (int i = 0; i < V; ++i) y[i] *= z[i];
+        }
         Row<V> o;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          y[i] = fmaf(D[i], get(x, i), y[i]);
-          if (zp) y[i] *= silu(get(z, i));
-          put(o, i, y[i]);
-        }
+        for (int i = 0; i < V; ++i) put(o, i, y[i]);
         if (c_blk + kc < a.d && t0 + t < t_end) store(yp + (t0 + t) * a.sy.t + kc, o);
       }
     }
