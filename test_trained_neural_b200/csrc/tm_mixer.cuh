@@ -228,6 +228,49 @@ __device__ __forceinline__ void values(float (&v)[V], const T *p) {
   for (int i = 0; i < V; ++i) v[i] = get(q, i);
 }
 
+// V values as pairs (a single value is in both halves of its pair)
+template <int V>
+using Pairs = F2[(V + 1) / 2];
+template <int V>
+__device__ __forceinline__ void to_pairs(Pairs<V> &r, const float (&v)[V]) {
+#pragma unroll
+  for (int i = 0; i < (V + 1) / 2; ++i) r[i] = pair(v[2 * i], v[V == 1 ? 0 : 2 * i + 1]);
+}
+template <int V>
+__device__ __forceinline__ void of_pairs(float (&v)[V], const Pairs<V> &r) {
+#pragma unroll
+  for (int i = 0; i < (V + 1) / 2; ++i) {
+    float b;
+    unpair(v[2 * i], b, r[i]);
+    if (V > 1) v[V == 1 ? 0 : 2 * i + 1] = b;
+  }
+}
+template <int V>
+__device__ __forceinline__ void lds(Pairs<V> &r, const float *p) {
+  float v[V];
+  lds<V>(v, p);
+  to_pairs<V>(r, v);
+}
+template <int V>
+__device__ __forceinline__ void sts(float *p, const Pairs<V> &r) {
+  float v[V];
+  of_pairs<V>(v, r);
+  sts<V>(p, v);
+}
+template <typename T, int V>
+__device__ __forceinline__ void values(Pairs<V> &r, const T *p) {
+  float v[V];
+  values<T, V>(v, p);
+  to_pairs<V>(r, v);
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_pairs(T *p, const Pairs<V> &r) {
+  Row<V> o;
+  of_pairs<V>(o.f, r);
+  store(p, o);
+}
+__device__ __forceinline__ F2 keep_if(F2 x, bool live) { return live ? x : both(0.f); }
+
 // Tokens of sequence b: the caller's length held to [0, T].
 __device__ __forceinline__ int tokens_of(const int *lengths, int b, int T) {
   return lengths ? min(max(lengths[b], 0), T) : T;

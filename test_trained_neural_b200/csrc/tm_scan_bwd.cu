@@ -6,9 +6,9 @@
 //   dz_t = dy_t silu'(z_t) (sum_n Cm_t h_t + D x_t),  dD = sum_{b,t} k_t x_t
 //
 // Two passes over the tokens. The first walks forward and keeps the state at
-// every 8th token (fp32). The second walks the 8-token tiles backward: from a
-// kept state it forms the tile's 8 decays and states again, holds both in
-// registers (2 channels x 4 states x 8 tokens a lane), and takes the tile's
+// every 4th token (fp32). The second walks backward in chunks of 4 tokens: from
+// a kept state it forms the chunk's 4 decays and states again, holds both in
+// registers (2 channels x 4 states x 4 tokens a lane), and takes the chunk's
 // tokens in reverse. exp() is so evaluated twice per (token, channel, state)
 // in all, and no state is read back from memory but the kept ones.
 // When there are few channels the sequence is split into segments that both
@@ -23,7 +23,8 @@ namespace mix {
 namespace {
 
 using bf16 = __nv_bfloat16;
-constexpr int K = 8;                 // tokens between kept states
+constexpr int K = 4;                 // tokens between kept states
+constexpr int TS = 8;                // tokens of the second pass's tile
 constexpr int CPL = 2;               // channels of a lane
 constexpr int TF = 16;               // tokens of the first pass's tile
 constexpr int MAXW = 4;              // warps of a CTA
@@ -41,10 +42,10 @@ Plan plan_of(int B, int H, int G, int T, int d, int N) {
   p.NP = NL * SPL;
   p.warps = d <= 2 * CW ? 2 : MAXW;
   p.blocks = (d + CW * p.warps - 1) / (CW * p.warps);
-  // two CTAs of 4 warps fit on an SM; a split costs the first pass the
+  // three CTAs of 4 warps fit on an SM; a split costs the first pass the
   // gradient sums and the joins, so it has to at least double the CTAs
   const long long ctas = (long long)B * H * p.blocks * p.warps / MAXW + 1;
-  long long S = 2LL * kSMs / ctas;
+  long long S = 3LL * kSMs / ctas;
   const long long most = T / 64;
   if (S > most) S = most;
   if (S < 2) S = 1;
@@ -86,161 +87,217 @@ __device__ __forceinline__ Where where(const Scan &a, const Plan &pl) {
   return w;
 }
 
-// First pass: states at every K-th token.
-template <typename T, int NL, int V, bool SPLIT>
-__global__ void __launch_bounds__(32 * MAXW) states_kernel(const Scan a, const Plan pl, float *ws) {
-  constexpr int NP = NL * SPL, CW = 32 / NL * CPL;
-  constexpr int TILE = TF * CW / V;                     // vectors of a warp's share of a tile
-  constexpr int NV = TILE >= 32 ? TILE / 32 : 1;
+// First pass: states at every K-th token. Shared memory: raw tiles of x, dt (and
+// with SPLIT z, dy), twice; e, u = e x (and k) of the tile; B (and C), each value
+// twice side by side; the bias of the channels.
+template <typename T, int NL, int V, int W, bool SPLIT>
+struct StatesSmem {
+  static constexpr int NP = NL * SPL, CW = 32 / NL * CPL, CB = CW * W, Q = SPLIT ? 2 : 1;
+  static constexpr size_t floats = (1 + Q) * TF * CB + 2 * Q * TF * NP + CB;
+  static constexpr size_t bytes = floats * 4 + 2 * (2 * Q) * TF * CB * sizeof(T);
+};
+
+template <typename T, int NL, int V, int W, bool SPLIT>
+__global__ void __launch_bounds__(32 * W, 16 / W) states_kernel(const Scan a, const Plan pl, float *ws) {
+  using S = StatesSmem<T, NL, V, W, SPLIT>;
+  constexpr int NP = S::NP, CW = S::CW, CB = S::CB, Q = S::Q, nthr = 32 * W, P = (V + 1) / 2;
+  constexpr int NV = TF * CB / V / nthr;                // vectors of a tile a thread stages
+  constexpr int NB = (TF * NP + nthr - 1) / nthr;       // values of B a thread stages
+  static_assert(TF * CB / V % nthr == 0 && CPL == 2, "whole vectors for every thread; a lane's channels are one pair");
   extern __shared__ __align__(16) float sm[];
-  const int CB = CW * pl.warps;
-  float *s_e = sm, *s_u = s_e + TF * CB, *s_k = s_u + TF * CB, *s_B = s_k + (SPLIT ? TF * CB : 0), *s_C = s_B + TF * NP;
+  float *s_e = sm, *s_u = s_e + TF * CB, *s_k = s_u + TF * CB, *s_B = s_k + (SPLIT ? TF * CB : 0),
+        *s_C = s_B + 2 * TF * NP, *s_bias = s_B + 2 * Q * TF * NP;
+  T *s_raw = reinterpret_cast<T *>(s_bias + CB);        // [2][x, dt, z, dy][TF][CB]
   const Where w = where(a, pl);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, nl = lane % NL, cl = lane / NL;
-  const int nthr = 32 * pl.warps, n0 = nl * SPL, N = a.N;
+  const int n0 = nl * SPL, N = a.N;
   const int c_blk = w.cb * CB, c0 = warp * CW + cl * CPL;
   const long long bh = (long long)w.b * a.H + w.h;
   const int n_tok = tokens_of(a.lengths, w.b, a.T);
   const long long t_seg = (long long)w.seg * pl.L;
   const long long t_end = t_seg + pl.L < n_tok ? t_seg + pl.L : n_tok;
   const long long per = (long long)a.B * a.H * a.d, chan = bh * a.d + c_blk + c0;
+  const long long hd = (long long)w.h * a.d + c_blk;
   float *ck = ws + pl.ck, *cume = ws + pl.cume;
+  const bool idle = c_blk + warp * CW >= a.d;           // a warp beyond the head's channels only stages
 
-  float A2[CPL][SPL], hs[CPL][SPL], P[CPL][SPL], Gs[CPL][SPL], es[CPL];
-#pragma unroll
-  for (int c = 0; c < CPL; ++c) {
-    es[c] = 0.f;
-#pragma unroll
-    for (int s = 0; s < SPL; ++s) {
-      const bool live = c_blk + c0 + c < a.d && n0 + s < N;
-      A2[c][s] = live ? a.A[((long long)w.h * a.d + c_blk + c0 + c) * N + n0 + s] * kLog2e : 0.f;
-      hs[c][s] = live && a.state0 && w.seg == 0 ? a.state0[(chan + c) * N + n0 + s] : 0.f;
-      P[c][s] = 1.f;
-      Gs[c][s] = 0.f;
-    }
-  }
-  const int vpr = CB / V, vlog = __ffs(vpr) - 1, vtile = TF * vpr;
   const T *xp = static_cast<const T *>(a.x) + w.b * a.sx.b + w.h * a.sx.h + c_blk;
   const T *dp = static_cast<const T *>(a.dt) + w.b * a.sdt.b + w.h * a.sdt.h + c_blk;
   const T *zp = a.z ? static_cast<const T *>(a.z) + w.b * a.sz.b + w.h * a.sz.h + c_blk : nullptr;
   const T *yp = static_cast<const T *>(a.dy) + w.b * a.sdy.b + w.h * a.sdy.h + c_blk;
   const T *Bp = static_cast<const T *>(a.Bm) + w.b * a.sB.b + w.g * a.sB.h;
   const T *Cp = static_cast<const T *>(a.Cm) + w.b * a.sC.b + w.g * a.sC.h;
+  constexpr int vpr = CB / V;                           // vectors of a tile row
+  auto row_at = [&](int k) { return (tid + k * nthr) / vpr; };
+  auto col_at = [&](int k) { return (tid + k * nthr) % vpr * V; };
 
-  Vec<T, V> xr[NV], dr[NV], zr[NV], yr[NV];
-  auto fetch = [&](long long t0) {
+  T Br[NB], Cr[NB];
+  auto fetch = [&](long long t0, int buf) {
+    T *raw = s_raw + buf * 2 * Q * TF * CB;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int i = tid + k * nthr, c = (i & (vpr - 1)) * V;
-      const long long t = t0 + (i >> vlog);
-      const bool live = i < vtile && c_blk + c < a.d && t < t_end;
-      xr[k] = load_if<T, V>(xp + t * a.sx.t + c, live);
-      dr[k] = load_if<T, V>(dp + t * a.sdt.t + c, live);
-      if (SPLIT) {
-        zr[k] = load_if<T, V>(zp + t * a.sz.t + c, live && zp);
-        yr[k] = load_if<T, V>(yp + t * a.sdy.t + c, live);
-      }
+      const int r = row_at(k), c = col_at(k);
+      const long long t = t0 + r;
+      const bool live = c_blk + c < a.d && t < t_end;
+      T *to = raw + r * CB + c;
+      copy_in<T, V>(to, live ? xp + t * a.sx.t + c : xp, live);
+      copy_in<T, V>(to + TF * CB, live ? dp + t * a.sdt.t + c : dp, live);
+      if (SPLIT && zp) copy_in<T, V>(to + 2 * TF * CB, live ? zp + t * a.sz.t + c : zp, live);
+      if (SPLIT) copy_in<T, V>(to + 3 * TF * CB, live ? yp + t * a.sdy.t + c : yp, live);
+    }
+    copies_sent();
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+      const int i = tid + k * nthr, n = i % NP;
+      const long long t = t0 + i / NP;
+      const bool live = i < TF * NP && t < t_end && n < N;
+      Br[k] = live ? Bp[t * a.sB.t + n] : T(0.f);
+      if (SPLIT) Cr[k] = live ? Cp[t * a.sC.t + n] : T(0.f);
     }
   };
-  fetch(t_seg);
-  for (long long t0 = t_seg; t0 < t_end; t0 += TF) {
-    for (int i = tid; i < TF * NP; i += nthr) {
-      const int t = i / NP, n = i % NP;
-      const bool live = t0 + t < t_end && n < N;
-      s_B[i] = live ? to_f(Bp[(t0 + t) * a.sB.t + n]) : 0.f;
-      if (SPLIT) s_C[i] = live ? to_f(Cp[(t0 + t) * a.sC.t + n]) : 0.f;
+  fetch(t_seg, 0);
+  for (int i = tid; i < CB; i += nthr) s_bias[i] = c_blk + i < a.d && a.dt_bias ? a.dt_bias[hd + i] : 0.f;
+
+  F2 A2[SPL], hs[SPL], Pr[SPL], Gs[SPL], es = both(0.f);
+#pragma unroll
+  for (int s = 0; s < SPL; ++s) {
+    float A[CPL], h[CPL];
+#pragma unroll
+    for (int c = 0; c < CPL; ++c) {
+      const bool live = c_blk + c0 + c < a.d && n0 + s < N;
+      A[c] = live ? a.A[(hd + c0 + c) * N + n0 + s] * kLog2e : 0.f;
+      h[c] = live && a.state0 && w.seg == 0 ? a.state0[(chan + c) * N + n0 + s] : 0.f;
+    }
+    A2[s] = pair(A[0], A[1]);
+    hs[s] = pair(h[0], h[1]);
+    Pr[s] = both(1.f);
+    Gs[s] = both(0.f);
+  }
+  auto keep = [&](float *to, const F2 (&v)[SPL], long long at) {
+    float q[2][SPL];
+#pragma unroll
+    for (int s = 0; s < SPL; ++s) unpair(q[0][s], q[1][s], v[s]);
+#pragma unroll
+    for (int c = 0; c < CPL; ++c)
+      if (c_blk + c0 + c < a.d) sts<SPL>(to + (at + c) * NP + n0, q[c]);
+  };
+  auto keep_sum = [&](float *to, long long at) {
+    float q[2];
+    unpair(q[0], q[1], es);
+#pragma unroll
+    for (int c = 0; c < CPL; ++c)
+      if (nl == 0 && c_blk + c0 + c < a.d) to[at + c] = q[c];
+  };
+  __syncthreads();                                      // s_bias
+  int buf = 0;
+  for (long long t0 = t_seg; t0 < t_end; t0 += TF, buf ^= 1) {
+    const T *raw = s_raw + buf * 2 * Q * TF * CB;
+    copies_done();
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+      const int i = tid + k * nthr;
+      if (i < TF * NP) {
+        reinterpret_cast<float2 *>(s_B)[i] = make_float2(to_f(Br[k]), to_f(Br[k]));
+        if (SPLIT) reinterpret_cast<float2 *>(s_C)[i] = make_float2(to_f(Cr[k]), to_f(Cr[k]));
+      }
     }
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int i = tid + k * nthr, kc = (i & (vpr - 1)) * V, t = i >> vlog;
-      if (i >= vtile) continue;
+      const int t = row_at(k), kc = col_at(k), at = t * CB + kc;
       const bool live = c_blk + kc < a.d && t0 + t < t_end;
+      Pairs<V> x, e, v;
+      values<T, V>(x, raw + at);
+      values<T, V>(e, raw + TF * CB + at);
+      lds<V>(v, s_bias + kc);
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        float e = get(dr[k], j) + (live && a.dt_bias ? a.dt_bias[(long long)w.h * a.d + c_blk + kc + j] : 0.f);
-        if (a.softplus) e = softplus(e);
-        e = live ? e : 0.f;
-        s_e[t * CB + kc + j] = e;
-        s_u[t * CB + kc + j] = e * get(xr[k], j);
-        if (SPLIT) s_k[t * CB + kc + j] = get(yr[k], j) * (zp ? silu(get(zr[k], j)) : 1.f);
+      for (int j = 0; j < P; ++j) {
+        e[j] = add(e[j], v[j]);
+        if (a.softplus) e[j] = softplus(e[j]);
+        e[j] = keep_if(e[j], live);
+        x[j] = mul(x[j], e[j]);
+      }
+      sts<V>(s_e + at, e);
+      sts<V>(s_u + at, x);
+      if (SPLIT) {
+        values<T, V>(v, raw + 3 * TF * CB + at);
+        if (zp) {
+          values<T, V>(x, raw + 2 * TF * CB + at);
+#pragma unroll
+          for (int j = 0; j < P; ++j) v[j] = mul(v[j], silu(x[j]));
+        }
+        sts<V>(s_k + at, v);
       }
     }
     __syncthreads();
-    fetch(t0 + TF);
+    fetch(t0 + TF, buf ^ 1);
+    if (!idle)
 #pragma unroll
-    for (int t = 0; t < TF; ++t) {
-      if (t % K == 0 && t0 + t < t_end) {
-        const long long tile = (t0 + t) / K;
-#pragma unroll
-        for (int c = 0; c < CPL; ++c) {
-          if (c_blk + c0 + c >= a.d) continue;
-          const long long at = tile * per + chan + c;
-          *reinterpret_cast<float4 *>(ck + at * NP + n0) = make_float4(hs[c][0], hs[c][1], hs[c][2], hs[c][3]);
-          if (SPLIT && nl == 0) cume[at] = es[c];
+      for (int t = 0; t < TF; ++t) {
+        if (t % K == 0 && t0 + t < t_end) {
+          const long long at = (t0 + t) / K * per + chan;
+          keep(ck, hs, at);
+          if (SPLIT) keep_sum(cume, at);
         }
-      }
-      float e[CPL], u[CPL], k[CPL], B[SPL], C[SPL];
-      lds<CPL>(e, s_e + t * CB + c0);
-      lds<CPL>(u, s_u + t * CB + c0);
-      lds<SPL>(B, s_B + t * NP + n0);
-      if (SPLIT) {
-        lds<CPL>(k, s_k + t * CB + c0);
-        lds<SPL>(C, s_C + t * NP + n0);
-      }
-#pragma unroll
-      for (int c = 0; c < CPL; ++c) {
-        if (SPLIT) es[c] += e[c];
+        float e[CPL], u[CPL], kf[CPL], B[2 * SPL], C[2 * SPL];
+        lds<CPL>(e, s_e + t * CB + c0);
+        lds<CPL>(u, s_u + t * CB + c0);
+        lds<2 * SPL>(B, s_B + (t * NP + n0) * 2);
+        if (SPLIT) {
+          lds<CPL>(kf, s_k + t * CB + c0);
+          lds<2 * SPL>(C, s_C + (t * NP + n0) * 2);
+        }
+        const F2 ee = pair(e[0], e[1]), uu = pair(u[0], u[1]);
+        if (SPLIT) es = add(es, ee);
 #pragma unroll
         for (int s = 0; s < SPL; ++s) {
-          const float av = ex2(e[c] * A2[c][s]);
-          hs[c][s] = fmaf(av, hs[c][s], u[c] * B[s]);
+          const F2 av = ex2(mul(ee, A2[s]));
+          hs[s] = fma(av, hs[s], mul(uu, pair(B[2 * s], B[2 * s + 1])));
           if (SPLIT) {
-            P[c][s] *= av;
-            Gs[c][s] = fmaf(P[c][s], C[s] * k[c], Gs[c][s]);
+            Pr[s] = mul(Pr[s], av);
+            Gs[s] = fma(Pr[s], mul(pair(C[2 * s], C[2 * s + 1]), pair(kf[0], kf[1])), Gs[s]);
           }
         }
       }
-    }
     __syncthreads();
   }
-  if (SPLIT)
-#pragma unroll
-    for (int c = 0; c < CPL; ++c) {
-      if (c_blk + c0 + c >= a.d) continue;
-      const long long at = w.seg * per + chan + c;
-      if (nl == 0) ws[pl.esum + at] = es[c];
-      *reinterpret_cast<float4 *>(ws + pl.hloc + at * NP + n0) = make_float4(hs[c][0], hs[c][1], hs[c][2], hs[c][3]);
-      *reinterpret_cast<float4 *>(ws + pl.gloc + at * NP + n0) = make_float4(Gs[c][0], Gs[c][1], Gs[c][2], Gs[c][3]);
-    }
+  copies_done();
+  if (SPLIT) {
+    keep(ws + pl.hloc, hs, w.seg * per + chan);
+    keep(ws + pl.gloc, Gs, w.seg * per + chan);
+    keep_sum(ws + pl.esum, w.seg * per + chan);
+  }
 }
 
 // Second pass: the gradients. Shared memory of a CTA of W warps: raw tiles of
 // x, dt, z, dy and the kept states, twice (the next tile is on its way); e, u =
-// e x and k of the tile; B and C, each value twice side by side; and what the
-// lanes add up to: per token the parts of sum_n g Bm, of sum_n A g a h and of
-// sum_n Cm h of each of the NL lanes of a channel, and each lane's parts of dB
-// and dC over its channels. Adding those up from shared memory takes half the
-// instructions of shuffles.
+// e x and k of the tile; B and C, each value twice side by side; the bias and D
+// of the channels; and, for the 4 tokens of a chunk, what the lanes add up to:
+// the parts of sum_n g Bm, of sum_n A g a h and of sum_n Cm h of each of the NL
+// lanes of a channel, and each lane's parts of dB and dC over its channels.
+// Adding those up from shared memory takes half the instructions of shuffles.
 template <typename T, int NL, int V, int W>
 struct GradSmem {
-  static constexpr int NP = NL * SPL, CW = 32 / NL * CPL, CB = CW * W, CS = CB + 8;
-  static constexpr size_t floats = 3 * K * CB + 4 * K * NP + 2 * CB * NP + 3 * K * NL * CS + 2 * K * W * 128;
-  static constexpr size_t bytes = floats * 4 + 8 * K * CB * sizeof(T);
+  static constexpr int NP = NL * SPL, CW = 32 / NL * CPL, CB = CW * W, CS = CB + 8, NC = TS / K;
+  static constexpr size_t floats =
+      3 * TS * CB + 4 * TS * NP + 2 * CB + 2 * NC * CB * NP + 3 * K * NL * CS + 2 * K * W * 128;
+  static constexpr size_t bytes = floats * 4 + 8 * TS * CB * sizeof(T);
 };
 
 template <typename T, int NL, int V, int W, bool SPLIT>
-__global__ void __launch_bounds__(32 * W, 8 / W) grad_kernel(const Scan a, const Plan pl, float *ws) {
+__global__ void __launch_bounds__(32 * W, 12 / W) grad_kernel(const Scan a, const Plan pl, float *ws) {
   using S = GradSmem<T, NL, V, W>;
-  constexpr int NP = S::NP, CW = S::CW, CB = S::CB, CS = S::CS, nthr = 32 * W;
-  constexpr int NV = (K * CB / V + nthr - 1) / nthr;    // vectors of a tile a thread stages
-  constexpr int NB = (K * NP + nthr - 1) / nthr;        // values of B a thread stages
+  constexpr int NP = S::NP, CW = S::CW, CB = S::CB, CS = S::CS, NC = S::NC, nthr = 32 * W, P = (V + 1) / 2;
+  constexpr int vpr = CB / V, vtile = TS * vpr;         // vectors of a tile row, of a tile
+  constexpr int NV = (vtile + nthr - 1) / nthr;         // vectors of a tile a thread stages
+  constexpr int NB = (TS * NP + nthr - 1) / nthr;       // values of B a thread stages
   static_assert(CPL == 2, "the lane's two channels are one pair");
   extern __shared__ __align__(16) float sm[];
-  float *s_e = sm, *s_u = s_e + K * CB, *s_k = s_u + K * CB, *s_B = s_k + K * CB, *s_C = s_B + 2 * K * NP,
-        *s_ck = s_C + 2 * K * NP,                       // [2][warp][channel of the lane][lane]{4}
-        *s_un = s_ck + 2 * CB * NP,                     // [K][3][NL][CS]
+  float *s_e = sm, *s_u = s_e + TS * CB, *s_k = s_u + TS * CB, *s_B = s_k + TS * CB, *s_C = s_B + 2 * TS * NP,
+        *s_bias = s_C + 2 * TS * NP, *s_D = s_bias + CB,
+        *s_ck = s_D + CB,                               // [2][NC][warp][channel of the lane][lane]{4}
+        *s_un = s_ck + 2 * NC * CB * NP,                // [K][3][NL][CS]
         *s_bc = s_un + 3 * K * NL * CS;                 // [K][W][dB, dC][lane]{4}
-  T *s_raw = reinterpret_cast<T *>(s_bc + 2 * K * W * 128);   // [2][x, dt, z, dy][K][CB]
+  T *s_raw = reinterpret_cast<T *>(s_bc + 2 * K * W * 128);   // [2][x, dt, z, dy][TS][CB]
   const Where w = where(a, pl);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, nl = lane % NL, cl = lane / NL;
   const int n0 = nl * SPL, N = a.N;
@@ -265,19 +322,18 @@ __global__ void __launch_bounds__(32 * W, 8 / W) grad_kernel(const Scan a, const
   T *dzp = a.dz ? static_cast<T *>(a.dz) + w.b * a.sdz.b + w.h * a.sdz.h + c_blk : nullptr;
   float *bc = ws + pl.bc + ((((long long)(w.h % (a.H / a.G)) * pl.blocks + w.cb) * a.B + w.b) * a.G + w.g) * a.T * 2 * NP;
 
-  constexpr int vpr = CB / V, vtile = K * vpr;          // vectors of a tile row, of a tile
   auto row_at = [&](int k) { return (tid + k * nthr) / vpr; };
   auto col_at = [&](int k) { return (tid + k * nthr) % vpr * V; };
   auto in_tile = [&](int k) { return vtile % nthr == 0 || tid + k * nthr < vtile; };
 
   T Br[NB], Cr[NB];
-  float cu[CPL] = {0.f, 0.f};
+  float cu[NC][CPL];
   auto fetch = [&](long long t0, int buf) {
     if (t0 < t_seg || t0 >= n_tok) {
       copies_sent();
       return;
     }
-    T *raw = s_raw + buf * 4 * K * CB;
+    T *raw = s_raw + buf * 4 * TS * CB;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       if (!in_tile(k)) continue;
@@ -286,29 +342,31 @@ __global__ void __launch_bounds__(32 * W, 8 / W) grad_kernel(const Scan a, const
       const bool live = c_blk + c < a.d && t < n_tok;
       T *to = raw + r * CB + c;
       copy_in<T, V>(to, live ? xp + t * a.sx.t + c : xp, live);
-      copy_in<T, V>(to + K * CB, live ? dp + t * a.sdt.t + c : dp, live);
-      if (zp) copy_in<T, V>(to + 2 * K * CB, live ? zp + t * a.sz.t + c : zp, live);
-      copy_in<T, V>(to + 3 * K * CB, live ? yp + t * a.sdy.t + c : yp, live);
+      copy_in<T, V>(to + TS * CB, live ? dp + t * a.sdt.t + c : dp, live);
+      if (zp) copy_in<T, V>(to + 2 * TS * CB, live ? zp + t * a.sz.t + c : zp, live);
+      copy_in<T, V>(to + 3 * TS * CB, live ? yp + t * a.sdy.t + c : yp, live);
     }
 #pragma unroll
-    for (int c = 0; c < CPL; ++c) {
-      const bool in = c_blk + c0 + c < a.d;
-      const long long at = t0 / K * per + chan + c;
-      copy_in<float, SPL>(s_ck + buf * CB * NP + ((warp * CPL + c) * 32 + lane) * SPL, in ? ck + at * NP + n0 : ck, in);
-      if (SPLIT && w.seg > 0) cu[c] = in ? cume[at] : 0.f;
-    }
+    for (int q = 0; q < NC; ++q)
+#pragma unroll
+      for (int c = 0; c < CPL; ++c) {
+        const bool in = c_blk + c0 + c < a.d && t0 + q * K < n_tok;
+        const long long at = (t0 / K + q) * per + chan + c;
+        copy_in<float, SPL>(s_ck + (buf * NC + q) * CB * NP + ((warp * CPL + c) * 32 + lane) * SPL,
+                            in ? ck + at * NP + n0 : ck, in);
+        if (SPLIT && w.seg > 0) cu[q][c] = in ? cume[at] : 0.f;
+      }
     copies_sent();
 #pragma unroll
     for (int k = 0; k < NB; ++k) {
       const int i = tid + k * nthr, n = i % NP;
       const long long t = t0 + i / NP;
-      const bool live = i < K * NP && t < n_tok && n < N;
+      const bool live = i < TS * NP && t < n_tok && n < N;
       Br[k] = live ? Bp[t * a.sB.t + n] : T(0.f);
       Cr[k] = live ? Cp[t * a.sC.t + n] : T(0.f);
     }
   };
-  const long long tiles = (t_all - t_seg + K - 1) / K;
-  // entry i of a tile's [K][2 NP] sums: this CTA's partial, or the result where it is the only one
+  // entry i of a token's [2 NP] sums: this CTA's partial, or the result where it is the only one
   const long long row0 = ((long long)w.b * a.G + w.g) * a.T;
   auto out_bc = [&](long long t, int i, float s) {
     if (pl.pbn > 1) {
@@ -320,9 +378,9 @@ __global__ void __launch_bounds__(32 * W, 8 / W) grad_kernel(const Scan a, const
     }
   };
   // rows behind the sequence's end: zero gradients
-  long long tl = tiles - 1;
-  for (; tl >= 0 && t_seg + tl * K >= n_tok; --tl) {
-    const long long t0 = t_seg + tl * K;
+  long long tl = (t_all - t_seg + TS - 1) / TS - 1;
+  for (; tl >= 0 && t_seg + tl * TS >= n_tok; --tl) {
+    const long long t0 = t_seg + tl * TS;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int t = row_at(k), kc = col_at(k);
@@ -334,11 +392,16 @@ __global__ void __launch_bounds__(32 * W, 8 / W) grad_kernel(const Scan a, const
       store(ddp + (t0 + t) * a.sddt.t + kc, o);
       if (dzp) store(dzp + (t0 + t) * a.sdz.t + kc, o);
     }
-    for (int i = tid; i < K * 2 * NP; i += nthr)
+    for (int i = tid; i < TS * 2 * NP; i += nthr)
       if (t0 + i / (2 * NP) < t_all) out_bc(t0 + i / (2 * NP), i % (2 * NP), 0.f);
   }
   int buf = 0;
-  fetch(t_seg + tl * K, buf);
+  fetch(t_seg + tl * TS, buf);
+  for (int i = tid; i < CB; i += nthr) {
+    const bool in = c_blk + i < a.d;
+    s_bias[i] = in && a.dt_bias ? a.dt_bias[hd + i] : 0.f;
+    s_D[i] = in && a.D ? a.D[hd + i] : 0.f;
+  }
 
   F2 A2[SPL], R[SPL], dA[SPL], hin[SPL];
   {
@@ -377,23 +440,24 @@ __global__ void __launch_bounds__(32 * W, 8 / W) grad_kernel(const Scan a, const
       A2[s] = pair(Af[0][s], Af[1][s]);
       R[s] = pair(Rf[0][s], Rf[1][s]);
       hin[s] = pair(hf[0][s], hf[1][s]);
-      dA[s] = pair(0.f, 0.f);
+      dA[s] = both(0.f);
     }
   }
-  float sumD[NV][V], sumb[NV][V];
+  F2 sumD[NV][P], sumb[NV][P];
 #pragma unroll
   for (int k = 0; k < NV; ++k)
 #pragma unroll
-    for (int j = 0; j < V; ++j) sumD[k][j] = sumb[k][j] = 0.f;
+    for (int j = 0; j < P; ++j) sumD[k][j] = sumb[k][j] = both(0.f);
+  __syncthreads();                                      // s_bias, s_D
 
   for (; tl >= 0; --tl, buf ^= 1) {
-    const long long t0 = t_seg + tl * K;
-    const T *raw = s_raw + buf * 4 * K * CB;
+    const long long t0 = t_seg + tl * TS;
+    const T *raw = s_raw + buf * 4 * TS * CB;
     copies_done();
 #pragma unroll
     for (int k = 0; k < NB; ++k) {
       const int i = tid + k * nthr;
-      if (i < K * NP) {
+      if (i < TS * NP) {
         reinterpret_cast<float2 *>(s_B)[i] = make_float2(to_f(Br[k]), to_f(Br[k]));
         reinterpret_cast<float2 *>(s_C)[i] = make_float2(to_f(Cr[k]), to_f(Cr[k]));
       }
@@ -403,170 +467,199 @@ __global__ void __launch_bounds__(32 * W, 8 / W) grad_kernel(const Scan a, const
       if (!in_tile(k)) continue;
       const int t = row_at(k), kc = col_at(k), at = t * CB + kc;
       const bool live = c_blk + kc < a.d && t0 + t < n_tok;
-      const Vec<T, V> x = load_if<T, V>(raw + at, true), dt = load_if<T, V>(raw + K * CB + at, true);
-      const Vec<T, V> z = load_if<T, V>(raw + 2 * K * CB + at, zp != nullptr), dy = load_if<T, V>(raw + 3 * K * CB + at, true);
-      float e[V], u[V], kk[V];
+      Pairs<V> x, e, v;
+      values<T, V>(x, raw + at);
+      values<T, V>(e, raw + TS * CB + at);
+      lds<V>(v, s_bias + kc);
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        e[j] = get(dt, j) + (live && a.dt_bias ? a.dt_bias[hd + kc + j] : 0.f);
+      for (int j = 0; j < P; ++j) {
+        e[j] = add(e[j], v[j]);
         if (a.softplus) e[j] = softplus(e[j]);
-        e[j] = live ? e[j] : 0.f;
-        u[j] = e[j] * get(x, j);
-        kk[j] = get(dy, j) * (zp ? silu(get(z, j)) : 1.f);
+        e[j] = keep_if(e[j], live);
+        x[j] = mul(x[j], e[j]);
       }
       sts<V>(s_e + at, e);
-      sts<V>(s_u + at, u);
-      sts<V>(s_k + at, kk);
-    }
-    F2 h0[SPL];
-    {
-      float q0[SPL], q1[SPL];
-      lds<SPL>(q0, s_ck + buf * CB * NP + ((warp * CPL) * 32 + lane) * SPL);
-      lds<SPL>(q1, s_ck + buf * CB * NP + ((warp * CPL + 1) * 32 + lane) * SPL);
-      const F2 es = pair(cu[0], cu[1]);
+      sts<V>(s_u + at, x);
+      values<T, V>(v, raw + 3 * TS * CB + at);
+      if (zp) {
+        values<T, V>(x, raw + 2 * TS * CB + at);
 #pragma unroll
-      for (int s = 0; s < SPL; ++s) {
-        h0[s] = pair(q0[s], q1[s]);
-        if (SPLIT && w.seg > 0) h0[s] = fma(ex2(mul(A2[s], es)), hin[s], h0[s]);
+        for (int j = 0; j < P; ++j) v[j] = mul(v[j], silu(x[j]));
       }
+      sts<V>(s_k + at, v);
     }
+    F2 cum[NC];
+#pragma unroll
+    for (int q = 0; q < NC; ++q) cum[q] = pair(cu[q][0], cu[q][1]);
     __syncthreads();
-    fetch(t0 - K, buf ^ 1);
+    fetch(t0 - TS, buf ^ 1);
 
-    if (!idle) {
-      // the tile's decays and states again
-      F2 av[K][SPL], hv[K][SPL];
 #pragma unroll
-      for (int t = 0; t < K; ++t) {
-        float e[CPL], u[CPL], B[2 * SPL];
-        lds<CPL>(e, s_e + t * CB + c0);
-        lds<CPL>(u, s_u + t * CB + c0);
-        lds<2 * SPL>(B, s_B + (t * NP + n0) * 2);
-        const F2 ee = pair(e[0], e[1]), uu = pair(u[0], u[1]);
+    for (int q = NC - 1; q >= 0; --q) {                 // the chunks of the tile, last first
+      if (!idle) {
+        F2 h0[SPL];
+        float q0[SPL], q1[SPL];
+        const float *kept = s_ck + (buf * NC + q) * CB * NP + (warp * CPL * 32 + lane) * SPL;
+        lds<SPL>(q0, kept);
+        lds<SPL>(q1, kept + 32 * SPL);
 #pragma unroll
         for (int s = 0; s < SPL; ++s) {
-          av[t][s] = ex2(mul(ee, A2[s]));
-          hv[t][s] = fma(av[t][s], t ? hv[t ? t - 1 : 0][s] : h0[s], mul(uu, pair(B[2 * s], B[2 * s + 1])));
+          h0[s] = pair(q0[s], q1[s]);
+          if (SPLIT && w.seg > 0) h0[s] = fma(ex2(mul(A2[s], cum[q])), hin[s], h0[s]);
+        }
+        // the chunk's decays and states again
+        F2 av[K][SPL], hv[K][SPL];
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+          const int t = q * K + i;
+          float e[CPL], u[CPL], B[2 * SPL];
+          lds<CPL>(e, s_e + t * CB + c0);
+          lds<CPL>(u, s_u + t * CB + c0);
+          lds<2 * SPL>(B, s_B + (t * NP + n0) * 2);
+          const F2 ee = pair(e[0], e[1]), uu = pair(u[0], u[1]);
+#pragma unroll
+          for (int s = 0; s < SPL; ++s) {
+            av[i][s] = ex2(mul(ee, A2[s]));
+            hv[i][s] = fma(av[i][s], i ? hv[i ? i - 1 : 0][s] : h0[s], mul(uu, pair(B[2 * s], B[2 * s + 1])));
+          }
+        }
+#pragma unroll
+        for (int i = K - 1; i >= 0; --i) {
+          const int t = q * K + i;
+          float e[CPL], u[CPL], kf[CPL], B[2 * SPL], C[2 * SPL];
+          lds<CPL>(e, s_e + t * CB + c0);
+          lds<CPL>(u, s_u + t * CB + c0);
+          lds<CPL>(kf, s_k + t * CB + c0);
+          lds<2 * SPL>(B, s_B + (t * NP + n0) * 2);
+          lds<2 * SPL>(C, s_C + (t * NP + n0) * 2);
+          const F2 ee = pair(e[0], e[1]), uu = pair(u[0], u[1]), kk = pair(kf[0], kf[1]);
+          F2 un, de, y;
+          float dB[SPL], dC[SPL];
+#pragma unroll
+          for (int s = 0; s < SPL; ++s) {
+            const F2 BB = pair(B[2 * s], B[2 * s + 1]), CC = pair(C[2 * s], C[2 * s + 1]);
+            const F2 h = hv[i][s], hp = i ? hv[i ? i - 1 : 0][s] : h0[s];
+            const F2 g = fma(CC, kk, R[s]);
+            float lo, hi;
+            unpair(lo, hi, mul(kk, h));
+            dC[s] = lo + hi;
+            unpair(lo, hi, mul(g, uu));
+            dB[s] = lo + hi;
+            R[s] = mul(g, av[i][s]);
+            const F2 qq = mul(R[s], hp);
+            dA[s] = fma(qq, ee, dA[s]);
+            un = s ? fma(g, BB, un) : mul(g, BB);
+            de = s ? fma(qq, A2[s], de) : mul(qq, A2[s]);
+            y = s ? fma(CC, h, y) : mul(CC, h);
+          }
+          float o[CPL];
+          float *to = s_un + (i * 3 * NL + nl) * CS + c0;
+          unpair(o[0], o[1], un);
+          sts<CPL>(to, o);
+          unpair(o[0], o[1], de);
+          sts<CPL>(to + NL * CS, o);
+          if (zp) {
+            unpair(o[0], o[1], y);
+            sts<CPL>(to + 2 * NL * CS, o);
+          }
+          float *tb = s_bc + (i * W + warp) * 2 * 128 + lane * 4;
+          sts<SPL>(tb, dB);
+          sts<SPL>(tb + 128, dC);
         }
       }
+      __syncthreads();
+      // the thread that staged an element finishes its gradients
 #pragma unroll
-      for (int t = K - 1; t >= 0; --t) {
-        float e[CPL], u[CPL], kf[CPL], B[2 * SPL], C[2 * SPL];
-        lds<CPL>(e, s_e + t * CB + c0);
-        lds<CPL>(u, s_u + t * CB + c0);
-        lds<CPL>(kf, s_k + t * CB + c0);
-        lds<2 * SPL>(B, s_B + (t * NP + n0) * 2);
-        lds<2 * SPL>(C, s_C + (t * NP + n0) * 2);
-        const F2 ee = pair(e[0], e[1]), uu = pair(u[0], u[1]), kk = pair(kf[0], kf[1]);
-        F2 un, de, y;
-        float dB[SPL], dC[SPL];
+      for (int k = 0; k < NV; ++k) {
+        const int t = row_at(k), kc = col_at(k), at = t * CB + kc;
+        if (!in_tile(k) || t / K != q || c_blk + kc >= a.d || t0 + t >= t_all) continue;
+        const bool live = t0 + t < n_tok;
+        Pairs<V> x, e, kk, D, du, de, yv, r;
 #pragma unroll
-        for (int s = 0; s < SPL; ++s) {
-          const F2 BB = pair(B[2 * s], B[2 * s + 1]), CC = pair(C[2 * s], C[2 * s + 1]);
-          const F2 h = hv[t][s], hp = t ? hv[t ? t - 1 : 0][s] : h0[s];
-          const F2 g = fma(CC, kk, R[s]);
-          float lo, hi;
-          unpair(lo, hi, mul(kk, h));
-          dC[s] = lo + hi;
-          unpair(lo, hi, mul(g, uu));
-          dB[s] = lo + hi;
-          R[s] = mul(g, av[t][s]);
-          const F2 q = mul(R[s], hp);
-          dA[s] = fma(q, ee, dA[s]);
-          un = s ? fma(g, BB, un) : mul(g, BB);
-          de = s ? fma(q, A2[s], de) : mul(q, A2[s]);
-          y = s ? fma(CC, h, y) : mul(CC, h);
+        for (int j = 0; j < P; ++j) du[j] = de[j] = yv[j] = both(0.f);
+#pragma unroll
+        for (int l = 0; l < NL; ++l) {
+          const float *from = s_un + (t % K * 3 * NL + l) * CS + kc;
+          lds<V>(r, from);
+#pragma unroll
+          for (int j = 0; j < P; ++j) du[j] = add(du[j], r[j]);
+          lds<V>(r, from + NL * CS);
+#pragma unroll
+          for (int j = 0; j < P; ++j) de[j] = add(de[j], r[j]);
+          if (zp) {
+            lds<V>(r, from + 2 * NL * CS);
+#pragma unroll
+            for (int j = 0; j < P; ++j) yv[j] = add(yv[j], r[j]);
+          }
         }
-        float o[CPL];
-        float *to = s_un + ((t * 3) * NL + nl) * CS + c0;
-        unpair(o[0], o[1], un);
-        sts<CPL>(to, o);
-        unpair(o[0], o[1], de);
-        sts<CPL>(to + NL * CS, o);
-        if (zp) {
-          unpair(o[0], o[1], y);
-          sts<CPL>(to + 2 * NL * CS, o);
+        values<T, V>(x, raw + at);
+        lds<V>(e, s_e + at);
+        lds<V>(kk, s_k + at);
+        lds<V>(D, s_D + kc);
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+          sumD[k][j] = fma(kk[j], x[j], sumD[k][j]);
+          r[j] = keep_if(fma(du[j], e[j], mul(D[j], kk[j])), live);
+          du[j] = fma(du[j], x[j], mul(de[j], both(1.f / kLog2e)));
         }
-        float *tb = s_bc + ((t * W + warp) * 2) * 128 + lane * 4;
-        sts<SPL>(tb, dB);
-        sts<SPL>(tb + 128, dC);
-      }
-    }
-    __syncthreads();
-    // the thread that staged an element finishes its gradients
+        store_pairs<T, V>(dxp + (t0 + t) * a.sdx.t + kc, r);
+        values<T, V>(r, raw + TS * CB + at);
+        lds<V>(e, s_bias + kc);
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int t = row_at(k), kc = col_at(k), at = t * CB + kc;
-      if (!in_tile(k) || c_blk + kc >= a.d || t0 + t >= t_all) continue;
-      const bool live = t0 + t < n_tok;
-      const Vec<T, V> xv = load_if<T, V>(raw + at, true), dtv = load_if<T, V>(raw + K * CB + at, true);
-      const Vec<T, V> zv = load_if<T, V>(raw + 2 * K * CB + at, zp != nullptr), dyv = load_if<T, V>(raw + 3 * K * CB + at, true);
-      float e[V], kk[V], du[V], de[V], yv[V];
-      lds<V>(e, s_e + at);
-      lds<V>(kk, s_k + at);
+        for (int j = 0; j < P; ++j) {
+          if (a.softplus) du[j] = mul(du[j], sigmoid(add(r[j], e[j])));
+          du[j] = keep_if(du[j], live);
+          sumb[k][j] = add(sumb[k][j], du[j]);
+        }
+        store_pairs<T, V>(ddp + (t0 + t) * a.sddt.t + kc, du);
+        if (dzp) {
+          values<T, V>(kk, raw + 2 * TS * CB + at);     // z, dy
+          values<T, V>(r, raw + 3 * TS * CB + at);
 #pragma unroll
-      for (int j = 0; j < V; ++j) du[j] = de[j] = yv[j] = 0.f;
-#pragma unroll
-      for (int l = 0; l < NL; ++l) {
-        const float *from = s_un + ((t * 3) * NL + l) * CS + kc;
-        float q[V];
-        lds<V>(q, from);
-#pragma unroll
-        for (int j = 0; j < V; ++j) du[j] += q[j];
-        lds<V>(q, from + NL * CS);
-#pragma unroll
-        for (int j = 0; j < V; ++j) de[j] += q[j];
-        if (zp) {
-          lds<V>(q, from + 2 * NL * CS);
-#pragma unroll
-          for (int j = 0; j < V; ++j) yv[j] += q[j];
+          for (int j = 0; j < P; ++j) {
+            const F2 s = sigmoid(kk[j]), one = both(1.f);
+            const F2 ds = mul(s, fma(kk[j], add(one, mul(s, both(-1.f))), one));
+            r[j] = keep_if(mul(mul(r[j], ds), fma(D[j], x[j], yv[j])), live);
+          }
+          store_pairs<T, V>(dzp + (t0 + t) * a.sdz.t + kc, r);
         }
       }
-      Row<V> ox, od, oz;
+      // dB and dC of the chunk: PT threads add up the lanes that hold a (token,
+      // lane of states); where a chunk's elements are half of the threads', the others do
+      constexpr bool HALF = vtile == nthr && NC == 2 && W % 2 == 0;
+      constexpr int BT = HALF ? nthr / 2 : nthr;
+      constexpr int TASKS = 2 * K * NL, PT = BT / TASKS > 1 ? BT / TASKS : 1;
+      const int bt = HALF ? tid - (q ? 0 : nthr / 2) : tid;
+      if (!HALF || (bt >= 0 && bt < BT)) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float x = get(xv, j);
-        const float D = a.D ? a.D[hd + kc + j] : 0.f;
-        float dd = fmaf(du[j], x, de[j] * (1.f / kLog2e));
-        if (a.softplus) dd *= sigmoid(get(dtv, j) + (a.dt_bias ? a.dt_bias[hd + kc + j] : 0.f));
-        dd = live ? dd : 0.f;
-        put(ox, j, live ? fmaf(du[j], e[j], D * kk[j]) : 0.f);
-        put(od, j, dd);
-        if (zp) {
-          const float z = get(zv, j), q = sigmoid(z);
-          put(oz, j, live ? get(dyv, j) * (q * fmaf(z, 1.f - q, 1.f)) * fmaf(D, x, yv[j]) : 0.f);
-        }
-        sumD[k][j] = fmaf(kk[j], x, sumD[k][j]);
-        sumb[k][j] += dd;
-      }
-      store(dxp + (t0 + t) * a.sdx.t + kc, ox);
-      store(ddp + (t0 + t) * a.sddt.t + kc, od);
-      if (dzp) store(dzp + (t0 + t) * a.sdz.t + kc, oz);
-    }
-    // dB and dC of the tile: PT threads add up the lanes that hold a (token, lane of states)
-    constexpr int TASKS = 2 * K * NL, PT = nthr / TASKS > 1 ? nthr / TASKS : 1;
+        for (int i0 = 0; i0 < TASKS * PT; i0 += BT) {
+          const int id = i0 + bt, l = id % NL, part = id / NL % PT, th = id / (NL * PT), half = th % 2, t = th / 2;
+          F2 s0 = both(0.f), s1 = both(0.f);
 #pragma unroll
-    for (int i0 = 0; i0 < TASKS * PT; i0 += nthr) {
-      const int id = i0 + tid, l = id % NL, part = id / NL % PT, th = id / (NL * PT), half = th % 2, t = th / 2;
-      float s[SPL] = {0.f, 0.f, 0.f, 0.f};
+          for (int v = 0; v < W; ++v) {
+            if (c_blk + v * CW >= a.d) continue;        // an idle warp left nothing
 #pragma unroll
-      for (int q = 0; q < W; ++q) {
-        if (c_blk + q * CW >= a.d) continue;            // an idle warp left nothing
+            for (int c = 0; c < 32 / NL; c += PT) {
+              Pairs<SPL> r;
+              lds<SPL>(r, s_bc + ((t * W + v) * 2 + half) * 128 + ((c + part) * NL + l) * 4);
+              s0 = add(s0, r[0]);
+              s1 = add(s1, r[1]);
+            }
+          }
+          float s[SPL];
+          unpair(s[0], s[1], s0);
+          unpair(s[2], s[3], s1);
 #pragma unroll
-        for (int c = 0; c < 32 / NL; c += PT) {
-          float v[SPL];
-          lds<SPL>(v, s_bc + ((t * W + q) * 2 + half) * 128 + ((c + part) * NL + l) * 4);
+          for (int o = 1; o < PT; o *= 2)
 #pragma unroll
-          for (int j = 0; j < SPL; ++j) s[j] += v[j];
+            for (int j = 0; j < SPL; ++j) s[j] += __shfl_xor_sync(0xffffffffu, s[j], o * NL);
+          const long long at = t0 + q * K + t;
+          if (part == 0 && at < t_all)
+#pragma unroll
+            for (int j = 0; j < SPL; ++j) out_bc(at, half * NP + l * SPL + j, s[j]);
         }
       }
-#pragma unroll
-      for (int o = 1; o < PT; o *= 2)
-#pragma unroll
-        for (int j = 0; j < SPL; ++j) s[j] += __shfl_xor_sync(0xffffffffu, s[j], o * NL);
-      if (part == 0 && t0 + t < t_all)
-#pragma unroll
-        for (int j = 0; j < SPL; ++j) out_bc(t0 + t, half * NP + l * SPL + j, s[j]);
+      if (q) __syncthreads();                           // the next chunk writes the parts again
     }
   }
   copies_done();
@@ -601,7 +694,7 @@ __global__ void __launch_bounds__(32 * W, 8 / W) grad_kernel(const Scan a, const
       if (c_blk + c >= a.d) continue;
       float s = 0.f;
 #pragma unroll
-      for (int t = 0; t < K; ++t) s += s_e[t * CB + c];
+      for (int t = 0; t < TS; ++t) s += s_e[t * CB + c];
       ws[pl.pd + (part * 2 + p) * HD + hd + c] = s;
     }
   }
@@ -650,14 +743,18 @@ __global__ void __launch_bounds__(256) join_param_kernel(const Scan a, const Pla
 
 template <typename T, int NL, int VF, int VB, int W, bool SPLIT>
 cudaError_t run(const Scan &c, const Plan &p, cudaStream_t st) {
-  constexpr int NP = NL * SPL, CB = 32 / NL * CPL * W, thr = 32 * W;
+  constexpr int NP = NL * SPL, thr = 32 * W;
   float *ws = static_cast<float *>(c.ws);
   const long long grid = (long long)c.B * c.H * p.blocks * p.S;
   const long long nbc = (long long)c.B * c.G * c.T * 2 * NP;
   if (grid > 0x7fffffffLL || (nbc + 255) / 256 > 0x7fffffffLL) return cudaErrorInvalidValue;
-  const size_t sm1 = ((SPLIT ? 3 : 2) * TF * CB + 2 * TF * NP) * 4;
-  states_kernel<T, NL, VF, SPLIT><<<(unsigned)grid, thr, sm1, st>>>(c, p, ws);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = cudaSuccess;
+  constexpr size_t sm1 = StatesSmem<T, NL, VF, W, SPLIT>::bytes;
+  auto states = states_kernel<T, NL, VF, W, SPLIT>;
+  if (sm1 > 48 * 1024) e = cudaFuncSetAttribute(states, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm1);
+  if (e != cudaSuccess) return e;
+  states<<<(unsigned)grid, thr, sm1, st>>>(c, p, ws);
+  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   constexpr size_t sm2 = GradSmem<T, NL, VB, W>::bytes;
   auto grad = grad_kernel<T, NL, VB, W, SPLIT>;
@@ -687,15 +784,15 @@ cudaError_t plan_and_run(const Scan &c, cudaStream_t st) {
 
 template <typename T>
 cudaError_t dispatch(const Scan &c, cudaStream_t st) {
-  const int el = sizeof(T);
+  constexpr int el = sizeof(T), W16 = 16 / el;
   auto vec = [&](int V) {
     return fits(c.x, c.sx, c.d, V, el) && fits(c.dt, c.sdt, c.d, V, el) && fits(c.z, c.sz, c.d, V, el) &&
            fits(c.dy, c.sdy, c.d, V, el) && fits(c.dx, c.sdx, c.d, V, el) && fits(c.ddt, c.sddt, c.d, V, el) &&
            fits(c.dz, c.sdz, c.d, V, el);
   };
   switch (lanes_of(c.N)) {
-    case 2: return vec(4) ? plan_and_run<T, 2, 4, 4>(c, st) : plan_and_run<T, 2, 1, 1>(c, st);
-    case 4: return vec(4) ? plan_and_run<T, 4, 4, 4>(c, st) : plan_and_run<T, 4, 1, 1>(c, st);
+    case 2: return vec(W16) ? plan_and_run<T, 2, W16, 4>(c, st) : plan_and_run<T, 2, 1, 1>(c, st);
+    case 4: return vec(W16) ? plan_and_run<T, 4, W16, 4>(c, st) : plan_and_run<T, 4, 1, 1>(c, st);
     case 8: return vec(2) ? plan_and_run<T, 8, 2, 2>(c, st) : plan_and_run<T, 8, 1, 1>(c, st);
     case 16: return vec(2) ? plan_and_run<T, 16, 2, 1>(c, st) : plan_and_run<T, 16, 1, 1>(c, st);
     default: return plan_and_run<T, 32, 1, 1>(c, st);
