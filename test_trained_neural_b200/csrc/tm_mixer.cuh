@@ -270,6 +270,14 @@ __device__ __forceinline__ void store_pairs(T *p, const Pairs<V> &r) {
   store(p, o);
 }
 __device__ __forceinline__ F2 keep_if(F2 x, bool live) { return live ? x : both(0.f); }
+// ex2 whose value the compiler may not keep from an earlier one.
+__device__ __forceinline__ F2 ex2_again(F2 x) {
+  float a, b;
+  unpair(a, b, x);
+  asm volatile("ex2.approx.ftz.f32 %0, %0;" : "+f"(a));
+  asm volatile("ex2.approx.ftz.f32 %0, %0;" : "+f"(b));
+  return pair(a, b);
+}
 
 // Tokens of sequence b: the caller's length held to [0, T].
 __device__ __forceinline__ int tokens_of(const int *lengths, int b, int T) {

@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(32 * W, 12 / W) grad_kernel(const Scan a, cons
           if (SPLIT && w.seg > 0) h0[s] = fma(ex2(mul(A2[s], cum[q])), hin[s], h0[s]);
         }
         // the chunk's decays and states again
-        F2 av[K][SPL], hv[K][SPL];
+        F2 hv[K][SPL];
 #pragma unroll
         for (int i = 0; i < K; ++i) {
           const int t = q * K + i;
@@ -519,8 +519,7 @@ __global__ void __launch_bounds__(32 * W, 12 / W) grad_kernel(const Scan a, cons
           const F2 ee = pair(e[0], e[1]), uu = pair(u[0], u[1]);
 #pragma unroll
           for (int s = 0; s < SPL; ++s) {
-            av[i][s] = ex2(mul(ee, A2[s]));
-            hv[i][s] = fma(av[i][s], i ? hv[i ? i - 1 : 0][s] : h0[s], mul(uu, pair(B[2 * s], B[2 * s + 1])));
+            hv[i][s] = fma(ex2(mul(ee, A2[s])), i ? hv[i ? i - 1 : 0][s] : h0[s], mul(uu, pair(B[2 * s], B[2 * s + 1])));
           }
         }
 #pragma unroll
@@ -545,7 +544,7 @@ __global__ void __launch_bounds__(32 * W, 12 / W) grad_kernel(const Scan a, cons
             dC[s] = lo + hi;
             unpair(lo, hi, mul(g, uu));
             dB[s] = lo + hi;
-            R[s] = mul(g, av[i][s]);
+            R[s] = mul(g, ex2_again(mul(ee, A2[s])));
             const F2 qq = mul(R[s], hp);
             dA[s] = fma(qq, ee, dA[s]);
             un = s ? fma(g, BB, un) : mul(g, BB);
