@@ -127,7 +127,7 @@ __device__ __forceinline__ void sts(float *p, const float (&v)[V]) {
 }
 
 // Asynchronous copy of V elements into shared memory, zeros where not `live`
-// (nothing is read then). Pieces under 4 bytes have no asynchronous form and
+// (nothing is read then, so src may point anywhere). Pieces under 4 bytes have no asynchronous form and
 // are copied at once. A thread that reads only what it copied itself needs
 // copies_done() and no barrier.
 template <typename T, int V>

@@ -81,28 +81,45 @@ __global__ void __launch_bounds__(32 * W, (NL >= 16 ? 8 : 16) / W) scan_kernel(c
   const T *Bp = static_cast<const T *>(a.Bm) + b * a.sB.b + g * a.sB.h;
   const T *Cp = static_cast<const T *>(a.Cm) + b * a.sC.b + g * a.sC.h;
 
+  // Source pointers of the tile that is fetched next, moved on by a tile at a
+  // time: this thread's first vector of each tensor, its first value of B and C.
+  constexpr int RK = nthr / vpr > 0 ? nthr / vpr : 1;    // rows between a thread's vectors, if its column is fixed
+  constexpr bool FIXED = nthr % vpr == 0;
+  const int r0 = row_at(0), col0 = col_at(0);
+  const T *xf = xp + (t_seg + r0) * a.sx.t + col0, *df = dp + (t_seg + r0) * a.sdt.t + col0;
+  const T *zf = zp + (t_seg + r0) * a.sz.t + col0;
+  const int bn = tid % NP, bt = tid / NP;
+  constexpr int BK = nthr / NP > 0 ? nthr / NP : 1;      // as RK, FIXED, for B and C
+  constexpr bool BFIXED = nthr % NP == 0;
+  const T *Bf = Bp + (t_seg + bt) * a.sB.t + bn, *Cf = Cp + (t_seg + bt) * a.sC.t + bn;
   T Br[NB], Cr[NB];
   auto fetch = [&](long long t0, int buf) {
     T *raw = s_raw + buf * 3 * TQ * CB;
+    const int left = t_end - t0 < TQ ? (int)(t_end - t0) : TQ;      // tokens of the tile
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int r = row_at(k), c = col_at(k);
-      const long long t = t0 + r;
-      const bool live = c_blk + c < a.d && t < t_end;
+      const int r = FIXED ? r0 + k * RK : row_at(k), c = FIXED ? col0 : col_at(k);
+      const long long dr = FIXED ? k * RK : r - r0, dc = FIXED ? 0 : c - col0;
+      const bool live = c_blk + c < a.d && r < left;
       T *to = raw + r * CB + c;
-      copy_in<T, V>(to, live ? xp + t * a.sx.t + c : xp, live);
-      copy_in<T, V>(to + TQ * CB, live ? dp + t * a.sdt.t + c : dp, live);
-      if (!LOCAL && zp) copy_in<T, V>(to + 2 * TQ * CB, live ? zp + t * a.sz.t + c : zp, live);
+      copy_in<T, V>(to, xf + dr * a.sx.t + dc, live);
+      copy_in<T, V>(to + TQ * CB, df + dr * a.sdt.t + dc, live);
+      if (!LOCAL && zp) copy_in<T, V>(to + 2 * TQ * CB, zf + dr * a.sz.t + dc, live);
     }
     copies_sent();
+    xf += TQ * a.sx.t;
+    df += TQ * a.sdt.t;
+    zf += TQ * a.sz.t;
 #pragma unroll
     for (int k = 0; k < NB; ++k) {
-      const int i = tid + k * nthr, n = i % NP;
-      const long long t = t0 + i / NP;
-      const bool live = i < TQ * NP && t < t_end && n < N;
-      Br[k] = live ? Bp[t * a.sB.t + n] : T(0.f);
-      if (!LOCAL) Cr[k] = live ? Cp[t * a.sC.t + n] : T(0.f);
+      const int i = tid + k * nthr, t = BFIXED ? bt + k * BK : i / NP, n = BFIXED ? bn : i % NP;
+      const long long dt = BFIXED ? k * BK : t - bt, dn = BFIXED ? 0 : n - bn;
+      const bool live = t < left && n < N;               // left <= TQ: inside the tile
+      Br[k] = live ? Bf[dt * a.sB.t + dn] : T(0.f);
+      if (!LOCAL) Cr[k] = live ? Cf[dt * a.sC.t + dn] : T(0.f);
     }
+    Bf += TQ * a.sB.t;
+    Cf += TQ * a.sC.t;
   };
   fetch(t_seg, 0);
 

@@ -33,12 +33,14 @@ struct Plan {
   int warps, blocks, S, L;           // as in the forward
   int NP;                            // padded states
   size_t ck, cume, hloc, gloc, esum, bc, pa, pd, total;   // offsets into the workspace, in floats
+  bool wide_bc;                      // dB and dC take four states at once
   int pbn;                           // partials of dB and dC: (head of the group, channel block)
 };
 
 Plan plan_of(int B, int H, int G, int T, int d, int N) {
   const int NL = lanes_of(N), CW = 32 / NL * CPL;
   Plan p;
+  p.wide_bc = false;
   p.NP = NL * SPL;
   p.warps = d <= 2 * CW ? 2 : MAXW;
   p.blocks = (d + CW * p.warps - 1) / (CW * p.warps);
@@ -131,29 +133,43 @@ __global__ void __launch_bounds__(32 * W, 16 / W) states_kernel(const Scan a, co
   auto row_at = [&](int k) { return (tid + k * nthr) / vpr; };
   auto col_at = [&](int k) { return (tid + k * nthr) % vpr * V; };
 
+  // source pointers of the tile that is fetched next, moved on by a tile at a time
+  constexpr int RK = nthr / vpr;                        // rows between a thread's vectors
+  static_assert(nthr % vpr == 0 || V == 1, "a thread's vectors share a column");
+  constexpr bool FIXED = nthr % vpr == 0;
+  const int r0 = row_at(0), col0 = col_at(0), bn = tid % NP, bt = tid / NP;
+  const T *xf = xp + (t_seg + r0) * a.sx.t + col0, *df = dp + (t_seg + r0) * a.sdt.t + col0;
+  const T *zf = zp + (t_seg + r0) * a.sz.t + col0, *yf = yp + (t_seg + r0) * a.sdy.t + col0;
+  const T *Bf = Bp + (t_seg + bt) * a.sB.t + bn, *Cf = Cp + (t_seg + bt) * a.sC.t + bn;
   T Br[NB], Cr[NB];
   auto fetch = [&](long long t0, int buf) {
     T *raw = s_raw + buf * 2 * Q * TF * CB;
+    const int left = t_end - t0 < TF ? (int)(t_end - t0) : TF;      // tokens of the tile
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int r = row_at(k), c = col_at(k);
-      const long long t = t0 + r;
-      const bool live = c_blk + c < a.d && t < t_end;
+      const int r = FIXED ? r0 + k * RK : row_at(k), c = FIXED ? col0 : col_at(k);
+      const long long dr = FIXED ? k * RK : r - r0, dc = FIXED ? 0 : c - col0;
+      const bool live = c_blk + c < a.d && r < left;
       T *to = raw + r * CB + c;
-      copy_in<T, V>(to, live ? xp + t * a.sx.t + c : xp, live);
-      copy_in<T, V>(to + TF * CB, live ? dp + t * a.sdt.t + c : dp, live);
-      if (SPLIT && zp) copy_in<T, V>(to + 2 * TF * CB, live ? zp + t * a.sz.t + c : zp, live);
-      if (SPLIT) copy_in<T, V>(to + 3 * TF * CB, live ? yp + t * a.sdy.t + c : yp, live);
+      copy_in<T, V>(to, xf + dr * a.sx.t + dc, live);
+      copy_in<T, V>(to + TF * CB, df + dr * a.sdt.t + dc, live);
+      if (SPLIT && zp) copy_in<T, V>(to + 2 * TF * CB, zf + dr * a.sz.t + dc, live);
+      if (SPLIT) copy_in<T, V>(to + 3 * TF * CB, yf + dr * a.sdy.t + dc, live);
     }
     copies_sent();
+    xf += TF * a.sx.t;
+    df += TF * a.sdt.t;
+    zf += TF * a.sz.t;
+    yf += TF * a.sdy.t;
 #pragma unroll
     for (int k = 0; k < NB; ++k) {
-      const int i = tid + k * nthr, n = i % NP;
-      const long long t = t0 + i / NP;
-      const bool live = i < TF * NP && t < t_end && n < N;
-      Br[k] = live ? Bp[t * a.sB.t + n] : T(0.f);
-      if (SPLIT) Cr[k] = live ? Cp[t * a.sC.t + n] : T(0.f);
+      const int i = tid + k * nthr, t = i / NP, n = i % NP;
+      const bool live = t < left && n < N;              // left <= TF: inside the tile
+      Br[k] = live ? Bf[(t - bt) * a.sB.t + (n - bn)] : T(0.f);
+      if (SPLIT) Cr[k] = live ? Cf[(t - bt) * a.sC.t + (n - bn)] : T(0.f);
     }
+    Bf += TF * a.sB.t;
+    Cf += TF * a.sC.t;
   };
   fetch(t_seg, 0);
   for (int i = tid; i < CB; i += nthr) s_bias[i] = c_blk + i < a.d && a.dt_bias ? a.dt_bias[hd + i] : 0.f;
@@ -326,45 +342,64 @@ __global__ void __launch_bounds__(32 * W, 12 / W) grad_kernel(const Scan a, cons
   auto col_at = [&](int k) { return (tid + k * nthr) % vpr * V; };
   auto in_tile = [&](int k) { return vtile % nthr == 0 || tid + k * nthr < vtile; };
 
+  // source pointers of the tile that is fetched next, moved back by a tile at a time
+  long long tl = (t_all - t_seg + TS - 1) / TS - 1;     // last tile of the segment with tokens, once the loop below is done
   T Br[NB], Cr[NB];
   float cu[NC][CPL];
+  const int r0 = row_at(0), col0 = col_at(0), bn = tid % NP, bt = tid / NP;
+  const T *xf, *df, *zf, *yf, *Bf, *Cf;
+  const float *kf0;
+  auto fetch_from = [&](long long t0) {
+    xf = xp + (t0 + r0) * a.sx.t + col0;
+    df = dp + (t0 + r0) * a.sdt.t + col0;
+    zf = zp + (t0 + r0) * a.sz.t + col0;
+    yf = yp + (t0 + r0) * a.sdy.t + col0;
+    Bf = Bp + (t0 + bt) * a.sB.t + bn;
+    Cf = Cp + (t0 + bt) * a.sC.t + bn;
+    kf0 = ck + (t0 / K * per + chan) * NP + n0;
+  };
   auto fetch = [&](long long t0, int buf) {
     if (t0 < t_seg || t0 >= n_tok) {
       copies_sent();
       return;
     }
     T *raw = s_raw + buf * 4 * TS * CB;
+    const int left = n_tok - t0 < TS ? (int)(n_tok - t0) : TS;      // tokens of the tile
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       if (!in_tile(k)) continue;
       const int r = row_at(k), c = col_at(k);
-      const long long t = t0 + r;
-      const bool live = c_blk + c < a.d && t < n_tok;
+      const bool live = c_blk + c < a.d && r < left;
       T *to = raw + r * CB + c;
-      copy_in<T, V>(to, live ? xp + t * a.sx.t + c : xp, live);
-      copy_in<T, V>(to + TS * CB, live ? dp + t * a.sdt.t + c : dp, live);
-      if (zp) copy_in<T, V>(to + 2 * TS * CB, live ? zp + t * a.sz.t + c : zp, live);
-      copy_in<T, V>(to + 3 * TS * CB, live ? yp + t * a.sdy.t + c : yp, live);
+      copy_in<T, V>(to, xf + (r - r0) * a.sx.t + (c - col0), live);
+      copy_in<T, V>(to + TS * CB, df + (r - r0) * a.sdt.t + (c - col0), live);
+      if (zp) copy_in<T, V>(to + 2 * TS * CB, zf + (r - r0) * a.sz.t + (c - col0), live);
+      copy_in<T, V>(to + 3 * TS * CB, yf + (r - r0) * a.sdy.t + (c - col0), live);
     }
 #pragma unroll
     for (int q = 0; q < NC; ++q)
 #pragma unroll
       for (int c = 0; c < CPL; ++c) {
-        const bool in = c_blk + c0 + c < a.d && t0 + q * K < n_tok;
-        const long long at = (t0 / K + q) * per + chan + c;
+        const bool in = c_blk + c0 + c < a.d && q * K < left;
         copy_in<float, SPL>(s_ck + (buf * NC + q) * CB * NP + ((warp * CPL + c) * 32 + lane) * SPL,
-                            in ? ck + at * NP + n0 : ck, in);
-        if (SPLIT && w.seg > 0) cu[q][c] = in ? cume[at] : 0.f;
+                            kf0 + (q * per + c) * NP, in);
+        if (SPLIT && w.seg > 0) cu[q][c] = in ? cume[(t0 / K + q) * per + chan + c] : 0.f;
       }
     copies_sent();
 #pragma unroll
     for (int k = 0; k < NB; ++k) {
-      const int i = tid + k * nthr, n = i % NP;
-      const long long t = t0 + i / NP;
-      const bool live = i < TS * NP && t < n_tok && n < N;
-      Br[k] = live ? Bp[t * a.sB.t + n] : T(0.f);
-      Cr[k] = live ? Cp[t * a.sC.t + n] : T(0.f);
+      const int i = tid + k * nthr, t = i / NP, n = i % NP;
+      const bool live = t < left && n < N;              // left <= TS: inside the tile
+      Br[k] = live ? Bf[(t - bt) * a.sB.t + (n - bn)] : T(0.f);
+      Cr[k] = live ? Cf[(t - bt) * a.sC.t + (n - bn)] : T(0.f);
     }
+    xf -= TS * a.sx.t;
+    df -= TS * a.sdt.t;
+    zf -= TS * a.sz.t;
+    yf -= TS * a.sdy.t;
+    Bf -= TS * a.sB.t;
+    Cf -= TS * a.sC.t;
+    kf0 -= NC * per * NP;
   };
   // entry i of a token's [2 NP] sums: this CTA's partial, or the result where it is the only one
   const long long row0 = ((long long)w.b * a.G + w.g) * a.T;
@@ -378,7 +413,6 @@ __global__ void __launch_bounds__(32 * W, 12 / W) grad_kernel(const Scan a, cons
     }
   };
   // rows behind the sequence's end: zero gradients
-  long long tl = (t_all - t_seg + TS - 1) / TS - 1;
   for (; tl >= 0 && t_seg + tl * TS >= n_tok; --tl) {
     const long long t0 = t_seg + tl * TS;
 #pragma unroll
@@ -396,6 +430,7 @@ __global__ void __launch_bounds__(32 * W, 12 / W) grad_kernel(const Scan a, cons
       if (t0 + i / (2 * NP) < t_all) out_bc(t0 + i / (2 * NP), i % (2 * NP), 0.f);
   }
   int buf = 0;
+  fetch_from(t_seg + tl * TS);
   fetch(t_seg + tl * TS, buf);
   for (int i = tid; i < CB; i += nthr) {
     const bool in = c_blk + i < a.d;
@@ -653,9 +688,19 @@ __global__ void __launch_bounds__(32 * W, 12 / W) grad_kernel(const Scan a, cons
 #pragma unroll
             for (int j = 0; j < SPL; ++j) s[j] += __shfl_xor_sync(0xffffffffu, s[j], o * NL);
           const long long at = t0 + q * K + t;
-          if (part == 0 && at < t_all)
+          if (part == 0 && at < t_all) {
+            if (pl.pbn > 1) {
+              sts<SPL>(bc + at * 2 * NP + half * NP + l * SPL, s);
+            } else if (pl.wide_bc) {
+              Row<SPL> o;
 #pragma unroll
-            for (int j = 0; j < SPL; ++j) out_bc(at, half * NP + l * SPL + j, s[j]);
+              for (int j = 0; j < SPL; ++j) put(o, j, s[j]);
+              if (l * SPL < N) store(static_cast<T *>(half ? a.dC : a.dB) + (row0 + at) * N + l * SPL, o);
+            } else {
+#pragma unroll
+              for (int j = 0; j < SPL; ++j) out_bc(at, half * NP + l * SPL + j, s[j]);
+            }
+          }
         }
       }
       if (q) __syncthreads();                           // the next chunk writes the parts again
@@ -776,7 +821,9 @@ cudaError_t run(const Scan &c, const Plan &p, cudaStream_t st) {
 
 template <typename T, int NL, int VF, int VB>
 cudaError_t plan_and_run(const Scan &c, cudaStream_t st) {
-  const Plan p = plan_of(c.B, c.H, c.G, c.T, c.d, c.N);
+  Plan p = plan_of(c.B, c.H, c.G, c.T, c.d, c.N);
+  p.wide_bc = c.N % SPL == 0 && reinterpret_cast<uintptr_t>(c.dB) % (SPL * sizeof(T)) == 0 &&
+              reinterpret_cast<uintptr_t>(c.dC) % (SPL * sizeof(T)) == 0;
   if (p.warps == 2) return p.S > 1 ? run<T, NL, VF, VB, 2, true>(c, p, st) : run<T, NL, VF, VB, 2, false>(c, p, st);
   return p.S > 1 ? run<T, NL, VF, VB, 4, true>(c, p, st) : run<T, NL, VF, VB, 4, false>(c, p, st);
 }
