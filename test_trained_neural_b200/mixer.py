@@ -73,6 +73,10 @@ def _par(t, shape, dev):
     return t is None or (t.dtype is _F32 and t.get_device() == dev and t.shape == shape and t.is_contiguous())
 
 
+def _len(t, B, dev):
+    return t is None or (t.dtype is _I32 and t.get_device() == dev and t.shape == (B,) and t.is_contiguous())
+
+
 def _tok(t, shape, kind, dev):
     """A token tensor (strides are looked at by _strides), or absent."""
     return t is None or (t.dtype is kind and t.get_device() == dev and t.shape == shape)
@@ -132,8 +136,9 @@ def _here(x, stream):
     return stream is None and x.is_cuda and x.get_device() == torch.cuda.current_device()
 
 
-def _stream_of(dev):
-    return torch.cuda.current_stream(dev).cuda_stream
+# the current stream's handle, without a Stream object around it where torch offers that
+_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _fresh(like, lengths, dtype=None):
@@ -158,11 +163,18 @@ def _workspace(given, x, fn, *sizes):
     return given, given.numel()
 
 
-def _conv_check(x, shape, filt, bias, hist, lengths, more):
-    w, dev, kind = filt.shape[-1], x.device, x.dtype
-    H, d = shape[1], shape[-1]
-    _check(dev, filt=(filt, (H, d, w), _F32, False), bias=(bias, (H, d), _F32, False),
-           hist=(hist, (shape[0], H, w - 1, d), kind, False), lengths=(lengths, (shape[0],), _I32, False), **more)
+def _conv_check(x, shape, filt, bias, hist, lengths, token2, tail):
+    """Checks what the three convolution calls share; the width."""
+    w, dev, kind = filt.shape[-1], x.get_device(), x.dtype
+    B, H, d = shape[0], shape[1], shape[-1]
+    past = (B, H, w - 1, d)
+    if not (_par(filt, (H, d, w), dev) and _par(bias, (H, d), dev) and _tok(token2, shape, kind, dev) and
+            _tok(hist, past, kind, dev) and (hist is None or hist.is_contiguous()) and
+            _tok(tail, past, kind, dev) and (tail is None or tail.is_contiguous()) and _len(lengths, B, dev)):
+        _check(x.device, filt=(filt, (H, d, w), _F32, False), bias=(bias, (H, d), _F32, False),
+               hist=(hist, past, kind, False), lengths=(lengths, (B,), _I32, False),
+               **{"out or dy": (token2, shape, kind, True), "tail or its gradient": (tail, past, kind, False)})
+    return w
 
 
 def short_conv(x, filt, bias=None, *, hist=None, lengths=None, act="silu", out=None, tail=None, stream=None):
@@ -175,13 +187,12 @@ def short_conv(x, filt, bias=None, *, hist=None, lengths=None, act="silu", out=N
         return _elsewhere(short_conv, stream, x, (filt, bias),
                           dict(hist=hist, lengths=lengths, act=act, out=out, tail=tail))
     shape = B, H, T, d = _shape("x", x, 4)
-    w, kind = filt.shape[-1], x.dtype
-    code, past = _dtype_code("x", x), (B, H, w - 1, d)
-    _conv_check(x, shape, filt, bias, hist, lengths, {"out": (out, shape, kind, True), "tail": (tail, past, kind, False)})
+    code = _dtype_code("x", x)
+    w = _conv_check(x, shape, filt, bias, hist, lengths, out, tail)
     if out is None:
         out = _fresh(x, lengths)
     if tail is None:
-        tail = x.new_empty(past)
+        tail = x.new_empty((B, H, w - 1, d))
     N.check(N.load().tm_conv(B, H, T, d, w, code, _named(_ACTS, "act", act), x.data_ptr(), filt.data_ptr(), _p(bias),
                              _p(hist), _p(lengths), out.data_ptr(), tail.data_ptr(), _strides("x out", x, out),
                              _stream_of(x.get_device())), "tm_conv")
@@ -196,10 +207,8 @@ def short_conv_backward(x, filt, dy, bias=None, *, hist=None, lengths=None, act=
         return _elsewhere(short_conv_backward, stream, x, (filt, dy, bias),
                           dict(hist=hist, lengths=lengths, act=act, dtail=dtail, workspace=workspace))
     shape = B, H, T, d = _shape("x", x, 4)
-    w, kind = filt.shape[-1], x.dtype
     code = _dtype_code("x", x)
-    _conv_check(x, shape, filt, bias, hist, lengths, {"dy": (dy, shape, kind, True),
-                                                      "dtail": (dtail, (B, H, w - 1, d), kind, False)})
+    w = _conv_check(x, shape, filt, bias, hist, lengths, dy, dtail)
     ws, n = _workspace(workspace, x, "tm_conv_backward_workspace_size", B, H, T, d, w, code)
     out = {"dx": torch.empty_like(x), "dfilt": torch.empty_like(filt)}
     if bias is not None:
@@ -219,16 +228,12 @@ def short_conv_step(x, hist, filt, bias=None, *, act="silu", out=None, stream=No
     if not _here(x, stream):
         return _elsewhere(short_conv_step, stream, x, (hist, filt, bias), dict(act=act, out=out))
     shape = B, H, d = _shape("x", x, 3)
-    w, kind, dev = filt.shape[-1], x.dtype, x.get_device()
     code = _dtype_code("x", x)
-    past = (B, H, w - 1, d)
-    if not (_par(filt, (H, d, w), dev) and _par(bias, (H, d), dev) and _tok(hist, past, kind, dev) and
-            hist.is_contiguous() and _tok(out, shape, kind, dev)):
-        _conv_check(x, shape, filt, bias, hist, None, {"out": (out, shape, kind, True)})
+    w = _conv_check(x, shape, filt, bias, hist, None, out, None)
     if out is None:
         out = x.new_empty(shape)
     N.check(N.load().tm_conv_step(B, H, d, w, code, _named(_ACTS, "act", act), x.data_ptr(), filt.data_ptr(), _p(bias),
-                                  hist.data_ptr(), out.data_ptr(), _strides("x out", x, out), _stream_of(dev)),
+                                  hist.data_ptr(), out.data_ptr(), _strides("x out", x, out), _stream_of(x.get_device())),
             "tm_conv_step")
     return out
 
@@ -248,7 +253,7 @@ def _scan_sizes(x, shape, dt, A, Bm, Cm, D, z, dt_bias, state, state2, token2, l
     if not (_tok(dt, shape, kind, dev) and _tok(z, shape, kind, dev) and _tok(token2, shape, kind, dev) and
             _tok(Bm, group, kind, dev) and _tok(Cm, group, kind, dev) and _par(A, (H, d, n), dev) and
             _par(D, par, dev) and _par(dt_bias, par, dev) and _par(state, held, dev) and _par(state2, held, dev) and
-            lengths is None):
+            _len(lengths, B, dev)):
         _check(x.device, dt=(dt, shape, kind, True), A=(A, (H, d, n), _F32, False), Bm=(Bm, group, kind, True),
                Cm=(Cm, group, kind, True), D=(D, par, _F32, False), z=(z, shape, kind, True),
                dt_bias=(dt_bias, par, _F32, False), state=(state, held, _F32, False),
@@ -331,11 +336,16 @@ def selective_scan_step(x, dt, A, Bm, Cm, state, *, D=None, z=None, dt_bias=None
     return out
 
 
-def _norm_check(x, shape, weight, bias, lengths, stats, over, more):
+def _norm_check(x, shape, weight, bias, lengths, stats, over, token2, kind):
+    """Checks what the two norm calls share; the shape of stats."""
     B, H, T, d = shape
+    dev, par = x.get_device(), (H, d)
     kept = (B, H, T, 2) if over == "token" else (B, H, 2)
-    _check(x.device, weight=(weight, (H, d), _F32, False), bias=(bias, (H, d), _F32, False),
-           lengths=(lengths, (B,), _I32, False), stats=(stats, kept, _F32, False), **more)
+    if not (_par(weight, par, dev) and _par(bias, par, dev) and _par(stats, kept, dev) and
+            _tok(token2, shape, kind, dev) and _len(lengths, B, dev)):
+        _check(x.device, weight=(weight, par, _F32, False), bias=(bias, par, _F32, False),
+               lengths=(lengths, (B,), _I32, False), stats=(stats, kept, _F32, False),
+               **{"out or dy": (token2, shape, kind, True)})
     return kept
 
 
@@ -358,11 +368,11 @@ def group_norm(x, weight=None, bias=None, *, over="token", act=None, eps=1e-5, l
     if kind not in _TYPES:
         raise TypeError(f"the output must be float32 or bfloat16, got {kind}")
     code, where = _dtype_code("x", x), _named(_OVER, "over", over)
-    kept = _norm_check(x, shape, weight, bias, lengths, stats, over, {"out": (out, shape, kind, True)})
+    kept = _norm_check(x, shape, weight, bias, lengths, stats, over, out, kind)
     if out is None:
         out = _fresh(x, lengths, kind)
     if stats is None:
-        stats = (x.new_empty if lengths is None else x.new_zeros)(kept, dtype=_F32)
+        stats = (x.new_empty if lengths is None or over == "sequence" else x.new_zeros)(kept, dtype=_F32)
     ws, n = _workspace(workspace, x, "tm_group_norm_workspace_size", B, H, T, d, where, 0)
     N.check(N.load().tm_group_norm(B, H, T, d, where, code, _TYPES[kind], _named(_ACTS, "act", act), float(eps),
                                    x.data_ptr(), _p(weight), _p(bias), _p(lengths), out.data_ptr(), stats.data_ptr(),
@@ -379,7 +389,7 @@ def group_norm_backward(x, dy, stats, weight=None, bias=None, *, over="token", a
                           dict(over=over, act=act, lengths=lengths, workspace=workspace))
     shape = B, H, T, d = _shape("x", x, 4)
     code, where, out_code = _dtype_code("x", x), _named(_OVER, "over", over), _dtype_code("dy", dy)
-    _norm_check(x, shape, weight, bias, lengths, stats, over, {"dy": (dy, shape, dy.dtype, True)})
+    _norm_check(x, shape, weight, bias, lengths, stats, over, dy, dy.dtype)
     ws, n = _workspace(workspace, x, "tm_group_norm_workspace_size", B, H, T, d, where, 1)
     out = {"dx": torch.empty_like(x)}
     if weight is not None:
