@@ -7,6 +7,8 @@
 // All of it is one pass over the tokens: the kernels are bound by HBM. A
 // thread owns V consecutive channels (16 bytes forward, 4 channels backward)
 // and a run of consecutive rows, whose w - 1 halo rows come from L1 and L2.
+#include <type_traits>
+
 #include "tm_mixer.cuh"
 
 namespace tmem {
@@ -14,6 +16,7 @@ namespace mix {
 namespace {
 
 constexpr int NT = 256;
+constexpr int BT = 128;              // threads of a gradient CTA
 using bf16 = __nv_bfloat16;
 
 // Channels of one (batch, head) in vectors of V, `nv` of them, walked in
@@ -41,49 +44,39 @@ __device__ __forceinline__ Vec<T, V> row_of(const T *x, long long st, const T *h
   return load_if<T, V>(hist + (w - 1 + t) * d, live && hist != nullptr && w - 1 + t >= 0);
 }
 
-// V floats at p, `live` or zeros; one 16-byte load where V is 4.
-template <int V>
-__device__ __forceinline__ void floats(float (&v)[V], const float *p, bool live) {
-  if (V == 4 && reinterpret_cast<uintptr_t>(p) % 16 == 0) {
-    const Vec<float, V> q = load_if<float, V>(p, live);
-#pragma unroll
-    for (int e = 0; e < V; ++e) v[e] = q.e[e];
-  } else {
-#pragma unroll
-    for (int e = 0; e < V; ++e) v[e] = live ? p[e] : 0.f;
-  }
-}
 // The filter taps and the bias of V channels, taps beyond the filter zero.
 template <int V, int MAXW>
-__device__ __forceinline__ void taps_of(float (&f)[MAXW][V], float (&bias)[V], const Conv &a, long long ch, bool live) {
+__device__ __forceinline__ void taps_of(Pairs<V> (&f)[MAXW], Pairs<V> &bias, const Conv &a, long long ch, bool live) {
   const float *fp = a.filt + ch * a.w;
-  if (MAXW == 4 && a.w == 4) {
+  float q[V][MAXW], bs[V];
+  const bool wide = MAXW == 4 && a.w == 4 && reinterpret_cast<uintptr_t>(fp) % 16 == 0;
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      float q[4];
-      floats<4>(q, fp + 4 * e, live);
+  for (int e = 0; e < V; ++e) {
+    bs[e] = live && a.bias ? a.bias[ch + e] : 0.f;
+    if (wide) {
+      const Vec<float, 4> v = load_if<float, 4>(fp + 4 * e, live);
 #pragma unroll
-      for (int j = 0; j < MAXW; ++j) f[j][e] = q[j & 3];
+      for (int j = 0; j < MAXW; ++j) q[e][j] = v.e[j & 3];
+    } else {
+#pragma unroll
+      for (int j = 0; j < MAXW; ++j) q[e][j] = live && j < a.w ? fp[e * a.w + j] : 0.f;
     }
-  } else {
-#pragma unroll
-    for (int e = 0; e < V; ++e)
-#pragma unroll
-      for (int j = 0; j < MAXW; ++j) f[j][e] = live && j < a.w ? fp[e * a.w + j] : 0.f;
   }
-  if (a.bias) {
-    floats<V>(bias, a.bias + ch, live);
-  } else {
+  to_pairs<V>(bias, bs);
 #pragma unroll
-    for (int e = 0; e < V; ++e) bias[e] = 0.f;
+  for (int j = 0; j < MAXW; ++j) {
+    float v[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) v[e] = q[e][j];
+    to_pairs<V>(f[j], v);
   }
 }
 
 // A thread walks `run` rows in batches of RB, the next batch's loads issued
 // before the current one is computed; the w - 1 rows before a batch stay in
 // registers, and the taps are read once for the whole run.
-template <typename T, int V, int MAXW, int RB>
-__global__ void __launch_bounds__(NT, MAXW <= 4 ? 3 : 2) conv_kernel(const Conv a, const Split sp, const int run) {
+template <typename T, int V, int MAXW, bool EXACT, int RB>
+__global__ void __launch_bounds__(NT, 2) conv_kernel(const Conv a, const Split sp, const int run) {
   unsigned blk = blockIdx.x;
   const int tile = blk % sp.tiles;
   blk /= sp.tiles;
@@ -107,39 +100,47 @@ __global__ void __launch_bounds__(NT, MAXW <= 4 ? 3 : 2) conv_kernel(const Conv 
   }
   if (t0 >= n) return;
 
-  Vec<T, V> raw[RB + MAXW - 1], next[RB];
+  constexpr int P = (V + 1) / 2;
+  Vec<T, V> next[RB];
+  Pairs<V> win[RB + MAXW - 1];                  // rows tb - (MAXW - 1) .. tb + RB - 1
 #pragma unroll
   for (int i = 0; i < MAXW - 1; ++i)
-    raw[i] = row_of<T, V>(x, a.sx.t, hist, w, d, t0 - (MAXW - 1) + i, i + w >= MAXW);
+    to_pairs<V>(win[i], row_of<T, V>(x, a.sx.t, hist, w, d, t0 - (MAXW - 1) + i, EXACT || i + w >= MAXW));
   const T *xp = x + t0 * a.sx.t;
 #pragma unroll
   for (int i = 0; i < RB; ++i) next[i] = load_if<T, V>(xp + i * a.sx.t, t0 + i < t1);
-  float f[MAXW][V], bias[V];
+  Pairs<V> f[MAXW], bias;
   taps_of<V, MAXW>(f, bias, a, (long long)h * d + c, true);
   T *y = static_cast<T *>(a.y) + b * a.sy.b + h * a.sy.h + c + t0 * a.sy.t;
-  for (long long tb = t0; tb < t1; tb += RB) {
+  // whole: every row of this batch, and of the next one that is fetched, is live
+  auto batch = [&](auto whole, int left) {
 #pragma unroll
-    for (int i = 0; i < RB; ++i) raw[MAXW - 1 + i] = next[i];
+    for (int i = 0; i < RB; ++i) to_pairs<V>(win[MAXW - 1 + i], next[i]);
     xp += RB * a.sx.t;
 #pragma unroll
-    for (int i = 0; i < RB; ++i) next[i] = load_if<T, V>(xp + i * a.sx.t, tb + RB + i < t1);
+    for (int i = 0; i < RB; ++i) next[i] = load_if<T, V>(xp + i * a.sx.t, whole || RB + i < left);
 #pragma unroll
     for (int r = 0; r < RB; ++r) {
-      Row<V> o;
+      Pairs<V> p;
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        float p = bias[e];
+      for (int e = 0; e < P; ++e) {
+        p[e] = bias[e];
 #pragma unroll
         for (int j = 0; j < MAXW; ++j)   // a tap beyond the filter is skipped: its row may hold an infinity
-          if (j < w) p = fmaf(f[j][e], get(raw[r + MAXW - 1 - j], e), p);
-        put(o, e, a.silu ? silu(p) : p);
+          if (EXACT || j < w) p[e] = fma(f[j][e], win[r + MAXW - 1 - j][e], p[e]);
+        if (a.silu) p[e] = silu(p[e]);
       }
-      if (tb + r < t1) store(y + r * a.sy.t, o);
+      if (whole || r < left) store_pairs<T, V>(y + r * a.sy.t, p);
     }
     y += RB * a.sy.t;
 #pragma unroll
-    for (int i = 0; i < MAXW - 1; ++i) raw[i] = raw[RB + i];
-  }
+    for (int i = 0; i < MAXW - 1; ++i)
+#pragma unroll
+      for (int e = 0; e < P; ++e) win[i][e] = win[RB + i][e];
+  };
+  int left = (int)(t1 - t0);
+  for (; left >= 2 * RB; left -= RB) batch(std::true_type{}, left);
+  for (; left > 0; left -= RB) batch(std::false_type{}, left);
 }
 
 // Gradients. A thread walks RB rows at a time through a run of `run` rows: it
@@ -149,9 +150,9 @@ __global__ void __launch_bounds__(NT, MAXW <= 4 ? 3 : 2) conv_kernel(const Conv 
 // groups of a CTA add theirs up in shared memory and the CTA writes one
 // partial, which a second launch sums in a fixed order (no atomics: the same
 // inputs give the same bits).
-template <typename T, int V, int MAXW, int RB>
-__global__ void __launch_bounds__(NT, 2) conv_backward_kernel(const Conv a, const Split sp, const int run, float *part) {
-  extern __shared__ float red[];               // [threads][V]
+template <typename T, int V, int MAXW, bool EXACT, int RB>
+__global__ void __launch_bounds__(BT, 3) conv_backward_kernel(const Conv a, const Split sp, const int run, float *part) {
+  extern __shared__ __align__(16) float red[];               // [threads][V]
   unsigned blk = blockIdx.x;
   const int tile = blk % sp.tiles;
   blk /= sp.tiles;
@@ -171,13 +172,14 @@ __global__ void __launch_bounds__(NT, 2) conv_backward_kernel(const Conv a, cons
   const T *dtail = a.dtail ? static_cast<const T *>(a.dtail) + bh * (w - 1) * d + c : nullptr;
   T *dhist = a.dhist ? static_cast<T *>(a.dhist) + bh * (w - 1) * d + c : nullptr;
 
-  float f[MAXW][V], bias[V], df[MAXW][V], db[V];
+  constexpr int P = (V + 1) / 2;
+  Pairs<V> f[MAXW], bias, df[MAXW], db;
   taps_of<V, MAXW>(f, bias, a, (long long)h * d + c, mine);
 #pragma unroll
-  for (int e = 0; e < V; ++e) {
-    db[e] = 0.f;
+  for (int e = 0; e < P; ++e) {
+    db[e] = both(0.f);
 #pragma unroll
-    for (int j = 0; j < MAXW; ++j) df[j][e] = 0.f;
+    for (int j = 0; j < MAXW; ++j) df[j][e] = both(0.f);
   }
   // This thread finishes the rows [t0, t1) of dx; rows -(w-1) .. -1 (the
   // history's) belong to the first run. It needs g of rows t0 .. t1 + w - 2
@@ -185,11 +187,10 @@ __global__ void __launch_bounds__(NT, 2) conv_backward_kernel(const Conv a, cons
   // the next one: they are whole batches, since RB divides the run.
   const long long t0 = ((long long)tile * sp.RL + rl) * run;
   const long long t1 = t0 + run < a.T ? t0 + run : a.T;
-  const long long first = t0 == 0 ? -(w - 1) : t0;
   if (mine && t0 < a.T) {
     const long long need = t1 + w - 1 < n ? t1 + w - 1 : n;     // rows of x and dy this run reads
-    Vec<T, V> xs[RB + MAXW - 1], xn[RB], dn[RB];
-    float g[RB + MAXW - 1][V];
+    Vec<T, V> xn[RB], dn[RB];
+    Pairs<V> xs[RB + MAXW - 1], g[RB + MAXW - 1];               // rows tb - (MAXW - 1) .. tb + RB - 1
     const T *xp = x + t0 * a.sx.t, *yp = dy + t0 * a.sdy.t;
 #pragma unroll
     for (int i = 0; i < RB; ++i) {
@@ -199,49 +200,48 @@ __global__ void __launch_bounds__(NT, 2) conv_backward_kernel(const Conv a, cons
 #pragma unroll
     for (int i = 0; i < MAXW - 1; ++i) {
       const long long t = t0 - (MAXW - 1) + i;
-      xs[i] = row_of<T, V>(x, a.sx.t, hist, w, d, t, i + w >= MAXW && t < n);
+      to_pairs<V>(xs[i], row_of<T, V>(x, a.sx.t, hist, w, d, t, (EXACT || i + w >= MAXW) && t < n));
 #pragma unroll
-      for (int e = 0; e < V; ++e) g[i][e] = 0.f;   // of rows this run does not finish, or before the call
+      for (int e = 0; e < P; ++e) g[i][e] = both(0.f);   // of rows this run does not finish, or before the call
     }
-    for (long long tb = t0; tb < t1 + MAXW - 1; tb += RB) {
-      Vec<T, V> dys[RB];
+    T *op = dx + (t0 - (MAXW - 1)) * a.sdx.t;
+    // One batch from row tb on. whole: every row that it reads, that it fetches
+    // and whose dx it finishes is live, inside the run, and short of the tail.
+    auto batch = [&](auto whole, long long tb) {
+      Pairs<V> dys[RB];
 #pragma unroll
       for (int i = 0; i < RB; ++i) {
-        xs[MAXW - 1 + i] = xn[i];
-        dys[i] = dn[i];
+        to_pairs<V>(xs[MAXW - 1 + i], xn[i]);
+        to_pairs<V>(dys[i], dn[i]);
       }
       xp += RB * a.sx.t;
       yp += RB * a.sdy.t;
 #pragma unroll
       for (int i = 0; i < RB; ++i) {
-        xn[i] = load_if<T, V>(xp + i * a.sx.t, tb + RB + i < need);
-        dn[i] = load_if<T, V>(yp + i * a.sdy.t, tb + RB + i < need);
+        xn[i] = load_if<T, V>(xp + i * a.sx.t, whole || tb + RB + i < need);
+        dn[i] = load_if<T, V>(yp + i * a.sdy.t, whole || tb + RB + i < need);
       }
-      const bool sums = tb < t1;
+      const bool sums = whole || tb < t1;
 #pragma unroll
       for (int i = 0; i < RB; ++i) {
-        const bool live = tb + i < need;
+        const bool live = whole || tb + i < need;
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          float xr[MAXW];
-#pragma unroll
-          for (int j = 0; j < MAXW; ++j) xr[j] = get(xs[MAXW - 1 + i - j], e);
-          float gg = get(dys[i], e);
+        for (int e = 0; e < P; ++e) {
+          F2 gg = dys[i][e];
           if (a.silu) {
-            float p = bias[e];
+            F2 p = bias[e];
 #pragma unroll
             for (int j = 0; j < MAXW; ++j)
-              if (j < w) p = fmaf(f[j][e], xr[j], p);
-            const float q = sigmoid(p);
-            gg *= q * fmaf(p, 1.f - q, 1.f);
+              if (EXACT || j < w) p = fma(f[j][e], xs[MAXW - 1 + i - j][e], p);
+            gg = mul(gg, silu_grad(p));
           }
-          gg = live ? gg : 0.f;
+          if (!live) gg = both(0.f);
           g[MAXW - 1 + i][e] = gg;
           if (sums && live) {
-            db[e] += gg;
+            db[e] = add(db[e], gg);
 #pragma unroll
             for (int j = 0; j < MAXW; ++j)
-              if (j < w) df[j][e] = fmaf(gg, xr[j], df[j][e]);
+              if (EXACT || j < w) df[j][e] = fma(gg, xs[MAXW - 1 + i - j][e], df[j][e]);
           }
         }
       }
@@ -249,43 +249,50 @@ __global__ void __launch_bounds__(NT, 2) conv_backward_kernel(const Conv a, cons
 #pragma unroll
       for (int i = 0; i < RB; ++i) {
         const long long t = tb - (MAXW - 1) + i;
-        if (t < first || t >= t1) continue;
-        float o[V];
+        if (!whole && (t < (t0 == 0 ? -(w - 1) : t0) || t >= t1)) continue;
+        Pairs<V> o;
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          o[e] = 0.f;
+        for (int e = 0; e < P; ++e) {
+          o[e] = mul(f[0][e], g[i][e]);
 #pragma unroll
-          for (int j = 0; j < MAXW; ++j)
-            if (j < w) o[e] = fmaf(f[j][e], g[i + j][e], o[e]);
+          for (int j = 1; j < MAXW; ++j)
+            if (EXACT || j < w) o[e] = fma(f[j][e], g[i + j][e], o[e]);
         }
-        // the tail's gradient: its row i' is row n - (w - 1) + i'
-        const long long k = t - ((long long)n - (w - 1));
-        if (dtail && k >= 0 && k < w - 1) {
-          const Vec<T, V> q = load_if<T, V>(dtail + k * d, true);
+        if (!whole) {
+          // the tail's gradient: its row i' is row n - (w - 1) + i'
+          const long long k = t - ((long long)n - (w - 1));
+          if (dtail && k >= 0 && k < w - 1) {
+            Pairs<V> q;
+            to_pairs<V>(q, load_if<T, V>(dtail + k * d, true));
 #pragma unroll
-          for (int e = 0; e < V; ++e) o[e] += get(q, e);
+            for (int e = 0; e < P; ++e) o[e] = add(o[e], q[e]);
+          }
+#pragma unroll
+          for (int e = 0; e < P; ++e) o[e] = keep_if(o[e], t < n);
         }
-        Row<V> q;
-#pragma unroll
-        for (int e = 0; e < V; ++e) put(q, e, t < n ? o[e] : 0.f);
-        if (t >= 0) store(dx + t * a.sdx.t, q);
-        else if (dhist) store(dhist + (w - 1 + t) * d, q);
+        if (whole || t >= 0) store_pairs<T, V>(op + i * a.sdx.t, o);
+        else if (dhist) store_pairs<T, V>(dhist + (w - 1 + t) * d, o);
       }
+      op += RB * a.sdx.t;
 #pragma unroll
-      for (int i = 0; i < MAXW - 1; ++i) {
-        xs[i] = xs[RB + i];
+      for (int i = 0; i < MAXW - 1; ++i)
 #pragma unroll
-        for (int e = 0; e < V; ++e) g[i][e] = g[RB + i][e];
-      }
-    }
+        for (int e = 0; e < P; ++e) {
+          xs[i][e] = xs[RB + i][e];
+          g[i][e] = g[RB + i][e];
+        }
+    };
+    long long tb = t0;
+    for (; tb < t0 + MAXW - 1; tb += RB) batch(std::false_type{}, tb);
+    for (; tb + 2 * RB <= need && tb + RB <= t1; tb += RB) batch(std::true_type{}, tb);
+    for (; tb < t1 + MAXW - 1; tb += RB) batch(std::false_type{}, tb);
   }
   // partial sums of the CTA: [b, tile][h, c, w + 1]
   float *out = part + (((long long)b * sp.tiles + tile) * a.H + h) * d * (w + 1);
 #pragma unroll
   for (int j = 0; j <= MAXW; ++j) {
     if (j < MAXW && j >= w) continue;
-#pragma unroll
-    for (int e = 0; e < V; ++e) red[threadIdx.x * V + e] = j < MAXW ? df[j < MAXW ? j : 0][e] : db[e];
+    sts<V>(red + threadIdx.x * V, j < MAXW ? df[j < MAXW ? j : 0] : db);
     __syncthreads();
     if (rl == 0 && mine) {
 #pragma unroll
@@ -365,7 +372,7 @@ BackPlan backward_plan(int B, int H, int T, int d, int V) {
   p.run = 128;
   const long long lanes = (long long)B * H * (d / V);
   while (p.run > 16 && lanes * ((T + p.run - 1) / p.run) < (long long)kSMs * 768) p.run /= 2;
-  p.sp = split_of(d, V, T, p.run, 64, NT);
+  p.sp = split_of(d, V, T, p.run, 32, BT);
   return p;
 }
 
@@ -402,12 +409,16 @@ cudaError_t conv_launch(Conv c, cudaStream_t st) {
     kern<<<(unsigned)grid, sp.nvb * sp.RL, 0, st>>>(c, sp, run);
     return cudaGetLastError();
   };
-  if (c.bf16) {
-    if (vec(4)) return c.w <= 4 ? go(conv_kernel<bf16, 4, 4, 8>, 4, 8) : go(conv_kernel<bf16, 4, 8, 8>, 4, 8);
-    return c.w <= 4 ? go(conv_kernel<bf16, 1, 4, 8>, 1, 8) : go(conv_kernel<bf16, 1, 8, 8>, 1, 8);
-  }
-  if (vec(4)) return c.w <= 4 ? go(conv_kernel<float, 4, 4, 4>, 4, 4) : go(conv_kernel<float, 4, 8, 4>, 4, 4);
-  return c.w <= 4 ? go(conv_kernel<float, 1, 4, 8>, 1, 8) : go(conv_kernel<float, 1, 8, 8>, 1, 8);
+  auto pick = [&](auto t, auto v) {
+    using T = decltype(t);
+    constexpr int V = decltype(v)::value;
+    if (c.w == 4) return go(conv_kernel<T, V, 4, true, 8>, V, 8);
+    if (c.w < 4) return go(conv_kernel<T, V, 4, false, 8>, V, 8);
+    return go(conv_kernel<T, V, 8, false, 4>, V, 4);
+  };
+  using std::integral_constant;
+  if (c.bf16) return vec(4) ? pick(bf16(), integral_constant<int, 4>()) : pick(bf16(), integral_constant<int, 1>());
+  return vec(4) ? pick(0.f, integral_constant<int, 4>()) : pick(0.f, integral_constant<int, 1>());
 }
 
 // The partials of conv_backward_kernel: the largest over the vector widths and
@@ -444,15 +455,14 @@ cudaError_t conv_backward_launch(Conv c, cudaStream_t st) {
     conv_sum_kernel<<<(unsigned)((n + 31) / 32), 256, 0, st>>>(part, c.B * sp.tiles, ch, c.w, c.dfilt, c.dbias);
     return cudaGetLastError();
   };
-  if (c.bf16) {
-#ifdef BV4
-    if (vec(4) && c.w <= 4) return go(conv_backward_kernel<bf16, 4, 4, 4>, 4);
-#endif
-    if (vec(2)) return c.w <= 4 ? go(conv_backward_kernel<bf16, 2, 4, 4>, 2) : go(conv_backward_kernel<bf16, 2, 8, 4>, 2);
-    return c.w <= 4 ? go(conv_backward_kernel<bf16, 1, 4, 4>, 1) : go(conv_backward_kernel<bf16, 1, 8, 4>, 1);
-  }
-  if (vec(2)) return c.w <= 4 ? go(conv_backward_kernel<float, 2, 4, 4>, 2) : go(conv_backward_kernel<float, 2, 8, 4>, 2);
-  return c.w <= 4 ? go(conv_backward_kernel<float, 1, 4, 4>, 1) : go(conv_backward_kernel<float, 1, 8, 4>, 1);
+  auto pick = [&](auto t) {
+    using T = decltype(t);
+    constexpr int W = sizeof(T) == 2 ? 4 : 2;
+    if (c.w == 4) return vec(W) ? go(conv_backward_kernel<T, W, 4, true, 4>, W) : go(conv_backward_kernel<T, 1, 4, true, 4>, 1);
+    if (c.w < 4) return vec(2) ? go(conv_backward_kernel<T, 2, 4, false, 4>, 2) : go(conv_backward_kernel<T, 1, 4, false, 4>, 1);
+    return vec(2) ? go(conv_backward_kernel<T, 2, 8, false, 4>, 2) : go(conv_backward_kernel<T, 1, 8, false, 4>, 1);
+  };
+  return c.bf16 ? pick(bf16()) : pick(0.f);
 }
 
 cudaError_t conv_step_launch(const Conv &c, cudaStream_t st) {

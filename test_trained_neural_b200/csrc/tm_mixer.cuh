@@ -269,6 +269,28 @@ __device__ __forceinline__ void store_pairs(T *p, const Pairs<V> &r) {
   of_pairs<V>(o.f, r);
   store(p, o);
 }
+// The values of a loaded vector, as pairs
+template <int V>
+__device__ __forceinline__ void to_pairs(Pairs<V> &r, const Vec<float, V> &q) {
+  to_pairs<V>(r, q.e);
+}
+template <int V>
+__device__ __forceinline__ void to_pairs(Pairs<V> &r, const Vec<__nv_bfloat16, V> &q) {
+#pragma unroll
+  for (int i = 0; i < (V + 1) / 2; ++i) r[i] = pair(get(q, 2 * i), get(q, V == 1 ? 0 : 2 * i + 1));
+}
+// What a pair adds up to (V = 1: one value)
+template <int V>
+__device__ __forceinline__ float total(F2 x) {
+  float a, b;
+  unpair(a, b, x);
+  return V == 1 ? a : a + b;
+}
+// silu'(p) = q (1 + p (1 - q)), q = sigmoid(p)
+__device__ __forceinline__ F2 silu_grad(F2 p) {
+  const F2 q = sigmoid(p), one = both(1.f);
+  return mul(q, fma(p, fma(q, both(-1.f), one), one));
+}
 __device__ __forceinline__ F2 keep_if(F2 x, bool live) { return live ? x : both(0.f); }
 // ex2 whose value the compiler may not keep from an earlier one.
 __device__ __forceinline__ F2 ex2_again(F2 x) {

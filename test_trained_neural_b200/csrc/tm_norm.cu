@@ -19,10 +19,22 @@ namespace {
 using bf16 = __nv_bfloat16;
 constexpr int NT = 256;
 
+// Sum over groups of LPR threads. Groups wider than a warp go through `red`
+// (NT / 32 floats) and a barrier: every thread of the CTA calls it, and the next
+// call uses another array.
 template <int LPR>
-__device__ __forceinline__ float lanes_sum(float x) {
+__device__ __forceinline__ float lanes_sum(float x, float *red = nullptr) {
 #pragma unroll
-  for (int o = LPR / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  for (int o = (LPR < 32 ? LPR : 32) / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  if constexpr (LPR > 32) {
+    constexpr int W = LPR / 32;
+    const int warp = threadIdx.x / 32;
+    if (threadIdx.x % 32 == 0) red[warp] = x;
+    __syncthreads();
+    x = 0.f;
+#pragma unroll
+    for (int i = 0; i < W; ++i) x += red[warp / W * W + i];
+  }
   return x;
 }
 // Sum over a CTA of NT threads; `red` holds NT / 32 floats.
@@ -43,27 +55,14 @@ __device__ __forceinline__ float act_grad(float p) {
 
 // weight and bias of V channels from hc on (1 and 0 where absent, or past the group).
 template <int V>
-__device__ __forceinline__ void affine_of(float (&w)[V], float (&bs)[V], const Norm &a, long long hc, bool live) {
+__device__ __forceinline__ void affine_of(Pairs<V> &w, Pairs<V> &bs, const Norm &a, long long hc, bool live) {
 #pragma unroll
-  for (int e = 0; e < V; ++e) {
-    w[e] = 1.f;
-    bs[e] = 0.f;
+  for (int e = 0; e < (V + 1) / 2; ++e) {
+    w[e] = both(1.f);
+    bs[e] = both(0.f);
   }
-  if (!live) return;
-  constexpr int P = V % 4 == 0 ? 4 : 1;                 // the launch checks their alignment
-#pragma unroll
-  for (int i = 0; i < V; i += P) {
-    if (a.weight) {
-      const Vec<float, P> q = load_if<float, P>(a.weight + hc + i, true);
-#pragma unroll
-      for (int e = 0; e < P; ++e) w[i + e] = q.e[e];
-    }
-    if (a.bias) {
-      const Vec<float, P> q = load_if<float, P>(a.bias + hc + i, true);
-#pragma unroll
-      for (int e = 0; e < P; ++e) bs[i + e] = q.e[e];
-    }
-  }
+  if (live && a.weight) lds<V>(w, a.weight + hc);        // the launch checks their alignment
+  if (live && a.bias) lds<V>(bs, a.bias + hc);
 }
 
 // ---- one token
@@ -71,60 +70,59 @@ __device__ __forceinline__ void affine_of(float (&w)[V], float (&bs)[V], const N
 // CTA: one (batch, head), NT / LPR rows side by side, RPT rows each.
 template <typename TI, typename TO, int V, int LPR, int IT, int RPT>
 __global__ void __launch_bounds__(NT) token_kernel(const Norm a, const int tiles) {
+  constexpr int P = (V + 1) / 2;
+  __shared__ float red[2][NT / 32];
   const int tile = blockIdx.x % tiles, bh = blockIdx.x / tiles;
   const int h = bh % a.H, b = bh / a.H, d = a.d;
   const int lane = threadIdx.x % LPR;
   const int n = tokens_of(a.lengths, b, a.T);
   const long long t0 = ((long long)tile * (NT / LPR) + threadIdx.x / LPR) * RPT;
-  const TI *x = static_cast<const TI *>(a.x) + b * a.sx.b + h * a.sx.h;
-  TO *y = static_cast<TO *>(a.y) + b * a.sy.b + h * a.sy.h;
+  const TI *x = static_cast<const TI *>(a.x) + b * a.sx.b + h * a.sx.h + t0 * a.sx.t + lane * V;
+  TO *y = static_cast<TO *>(a.y) + b * a.sy.b + h * a.sy.h + t0 * a.sy.t + lane * V;
   Vec<TI, V> raw[RPT][IT];
 #pragma unroll
   for (int r = 0; r < RPT; ++r)
 #pragma unroll
-    for (int i = 0; i < IT; ++i) {
-      const int c = (i * LPR + lane) * V;
-      raw[r][i] = load_if<TI, V>(x + (t0 + r) * a.sx.t + c, c < d && t0 + r < n);
-    }
-  float w[IT][V], bs[IT][V];
+    for (int i = 0; i < IT; ++i)
+      raw[r][i] = load_if<TI, V>(x + r * a.sx.t + i * LPR * V, (i * LPR + lane) * V < d && t0 + r < n);
+  Pairs<V> w[IT], bs[IT];
 #pragma unroll
   for (int i = 0; i < IT; ++i)
     affine_of<V>(w[i], bs[i], a, (long long)h * d + (i * LPR + lane) * V, (i * LPR + lane) * V < d);
   const float inv = 1.f / d;
 #pragma unroll
   for (int r = 0; r < RPT; ++r) {
-    float m = 0.f, q = 0.f;
+    Pairs<V> u[IT];
+    F2 s = both(0.f);
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+      to_pairs<V>(u[i], raw[r][i]);
+#pragma unroll
+      for (int e = 0; e < P; ++e) s = add(s, u[i][e]);          // lanes past d hold zeros
+    }
+    const float m = lanes_sum<LPR>(total<V>(s), red[0]) * inv;
+    s = both(0.f);
 #pragma unroll
     for (int i = 0; i < IT; ++i)
 #pragma unroll
-      for (int e = 0; e < V; ++e) m += get(raw[r][i], e);        // lanes past d hold zeros
-    m = lanes_sum<LPR>(m) * inv;
-#pragma unroll
-    for (int i = 0; i < IT; ++i)
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float u = (i * LPR + lane) * V < d ? get(raw[r][i], e) - m : 0.f;
-        q = fmaf(u, u, q);
+      for (int e = 0; e < P; ++e) {
+        u[i][e] = add(u[i][e], both(-m));
+        if ((i * LPR + lane) * V < d) s = fma(u[i][e], u[i][e], s);
       }
-    const float rs = rsqrtf(fmaf(lanes_sum<LPR>(q), inv, a.eps));
+    const float rs = rsqrtf(fmaf(lanes_sum<LPR>(total<V>(s), red[1]), inv, a.eps));
     const long long t = t0 + r;
     if (t >= n) continue;
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
-      const int c = (i * LPR + lane) * V;
-      if (c >= d) continue;
-      Row<V> o;
+      if ((i * LPR + lane) * V >= d) continue;
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float p = fmaf((get(raw[r][i], e) - m) * rs, w[i][e], bs[i][e]);
-        put(o, e, a.silu ? silu(p) : p);
+      for (int e = 0; e < P; ++e) {
+        u[i][e] = fma(mul(u[i][e], both(rs)), w[i][e], bs[i][e]);
+        if (a.silu) u[i][e] = silu(u[i][e]);
       }
-      store(y + t * a.sy.t + c, o);
+      store_pairs<TO, V>(y + r * a.sy.t + i * LPR * V, u[i]);
     }
-    if (a.stats && lane == 0) {
-      float2 *st = reinterpret_cast<float2 *>(a.stats) + ((long long)bh * a.T + t);
-      *st = make_float2(m, rs);
-    }
+    if (a.stats && lane == 0) reinterpret_cast<float2 *>(a.stats)[(long long)bh * a.T + t] = make_float2(m, rs);
   }
 }
 
@@ -161,22 +159,24 @@ __global__ void __launch_bounds__(NT) token_wide_kernel(const Norm a) {
 // summed in registers over all rows of the CTA.
 template <typename TI, typename TO, int V, int LPR, int IT, int RPT>
 __global__ void __launch_bounds__(NT) token_backward_kernel(const Norm a, const int tiles, float *part) {
-  extern __shared__ float red[];                        // [NT][V]
+  extern __shared__ __align__(16) float red[];          // [NT][V]
+  __shared__ float sums[2][NT / 32];
+  constexpr int ROWS = NT / LPR, P = (V + 1) / 2;
   const int tile = blockIdx.x % tiles, bh = blockIdx.x / tiles;
   const int h = bh % a.H, b = bh / a.H, d = a.d;
   const int lane = threadIdx.x % LPR, rg = threadIdx.x / LPR;
-  constexpr int ROWS = NT / LPR;
   const int n = tokens_of(a.lengths, b, a.T);
-  const TI *x = static_cast<const TI *>(a.x) + b * a.sx.b + h * a.sx.h;
-  const TO *dy = static_cast<const TO *>(a.dy) + b * a.sdy.b + h * a.sdy.h;
-  TI *dx = static_cast<TI *>(a.dx) + b * a.sdx.b + h * a.sdx.h;
-  const float2 *stats = reinterpret_cast<const float2 *>(a.stats) + (long long)bh * a.T;
-  float w[IT][V], bs[IT][V], dw[IT][V], db[IT][V];
+  const long long first = (long long)tile * ROWS * RPT + rg;
+  const TI *x = static_cast<const TI *>(a.x) + b * a.sx.b + h * a.sx.h + first * a.sx.t + lane * V;
+  const TO *dy = static_cast<const TO *>(a.dy) + b * a.sdy.b + h * a.sdy.h + first * a.sdy.t + lane * V;
+  TI *dx = static_cast<TI *>(a.dx) + b * a.sdx.b + h * a.sdx.h + first * a.sdx.t + lane * V;
+  const float2 *stats = reinterpret_cast<const float2 *>(a.stats) + (long long)bh * a.T + first;
+  Pairs<V> w[IT], bs[IT], dw[IT], db[IT];
 #pragma unroll
   for (int i = 0; i < IT; ++i) {
     affine_of<V>(w[i], bs[i], a, (long long)h * d + (i * LPR + lane) * V, (i * LPR + lane) * V < d);
 #pragma unroll
-    for (int e = 0; e < V; ++e) dw[i][e] = db[i][e] = 0.f;
+    for (int e = 0; e < P; ++e) dw[i][e] = db[i][e] = both(0.f);
   }
   const float inv = 1.f / d;
   const long long step = (long long)tiles * ROWS * RPT;
@@ -184,20 +184,24 @@ __global__ void __launch_bounds__(NT) token_backward_kernel(const Norm a, const 
   Vec<TI, V> xn[RPT][IT];
   Vec<TO, V> yn[RPT][IT];
   float2 sn[RPT];
-  auto fetch = [&](long long tb) {
+  auto fetch = [&](long long t0) {
 #pragma unroll
     for (int r = 0; r < RPT; ++r) {
-      const long long t = tb + r * ROWS + rg;
-      sn[r] = t < n ? stats[t] : make_float2(0.f, 0.f);
+      const bool live = t0 + r * ROWS < n;
+      sn[r] = live ? stats[r * ROWS] : make_float2(0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < IT; ++i) {
-        const int c = (i * LPR + lane) * V;
-        xn[r][i] = load_if<TI, V>(x + t * a.sx.t + c, c < d && t < n);
-        yn[r][i] = load_if<TO, V>(dy + t * a.sdy.t + c, c < d && t < n);
+        const bool in = (i * LPR + lane) * V < d && live;
+        xn[r][i] = load_if<TI, V>(x + r * ROWS * a.sx.t + i * LPR * V, in);
+        yn[r][i] = load_if<TO, V>(dy + r * ROWS * a.sdy.t + i * LPR * V, in);
       }
     }
+    x += step * a.sx.t;
+    dy += step * a.sdy.t;
+    stats += step;
   };
-  fetch((long long)tile * ROWS * RPT);
+  fetch(first);
+  // (the rows of a warp end together: every lane takes part in the sums)
   for (long long tb = (long long)tile * ROWS * RPT; tb < a.T; tb += step) {
     Vec<TI, V> xr[RPT][IT];
     Vec<TO, V> yr[RPT][IT];
@@ -211,41 +215,40 @@ __global__ void __launch_bounds__(NT) token_backward_kernel(const Norm a, const 
         yr[r][i] = yn[r][i];
       }
     }
-    fetch(tb + step);
+    fetch(tb + rg + step);
 #pragma unroll
     for (int r = 0; r < RPT; ++r) {
       const long long t = tb + r * ROWS + rg;
-      const float m = st[r].x, rs = st[r].y;
-      float k[IT][V], k1 = 0.f, k2 = 0.f;
-#pragma unroll
-      for (int i = 0; i < IT; ++i)
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float xh = (get(xr[r][i], e) - m) * rs;
-          float q = get(yr[r][i], e);                    // zero past d and past the sequence
-          if (a.silu) q *= act_grad(fmaf(xh, w[i][e], bs[i][e]));
-          db[i][e] += q;
-          dw[i][e] = fmaf(q, xh, dw[i][e]);
-          k[i][e] = q * w[i][e];
-          k1 += k[i][e];
-          k2 = fmaf(k[i][e], xh, k2);
-        }
-      k1 = lanes_sum<LPR>(k1) * inv;
-      k2 = lanes_sum<LPR>(k2) * inv;
-      if (t >= a.T) continue;
+      const F2 rs = both(st[r].y);
+      Pairs<V> k[IT], xh[IT];
+      F2 s1 = both(0.f), s2 = both(0.f);
 #pragma unroll
       for (int i = 0; i < IT; ++i) {
-        const int c = (i * LPR + lane) * V;
-        if (c >= d) continue;
-        Row<V> o;
+        to_pairs<V>(xh[i], xr[r][i]);
+        to_pairs<V>(k[i], yr[r][i]);                     // zero past d and past the sequence
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float xh = (get(xr[r][i], e) - m) * rs;
-          put(o, e, t < n ? rs * (k[i][e] - k1 - xh * k2) : 0.f);
+        for (int e = 0; e < P; ++e) {
+          xh[i][e] = mul(add(xh[i][e], both(-st[r].x)), rs);
+          if (a.silu) k[i][e] = mul(k[i][e], silu_grad(fma(xh[i][e], w[i][e], bs[i][e])));
+          db[i][e] = add(db[i][e], k[i][e]);
+          dw[i][e] = fma(k[i][e], xh[i][e], dw[i][e]);
+          k[i][e] = mul(k[i][e], w[i][e]);
+          s1 = add(s1, k[i][e]);
+          s2 = fma(k[i][e], xh[i][e], s2);
         }
-        store(dx + t * a.sdx.t + c, o);
+      }
+      const F2 k1 = both(-lanes_sum<LPR>(total<V>(s1), sums[0]) * inv), k2 = both(-lanes_sum<LPR>(total<V>(s2), sums[1]) * inv);
+      if (t < a.T) {
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+          if ((i * LPR + lane) * V >= d) continue;
+#pragma unroll
+          for (int e = 0; e < P; ++e) k[i][e] = mul(rs, fma(xh[i][e], k2, add(k[i][e], k1)));   // rs = 0 past the end
+          store_pairs<TI, V>(dx + r * ROWS * a.sdx.t + i * LPR * V, k[i]);
+        }
       }
     }
+    dx += step * a.sdx.t;
   }
   // partial of the CTA: [b, tile][2][h, c]
   float *out = part + ((long long)b * tiles + tile) * 2 * a.H * d + (long long)h * d;
@@ -253,8 +256,7 @@ __global__ void __launch_bounds__(NT) token_backward_kernel(const Norm a, const 
   for (int i = 0; i < IT; ++i)
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
-#pragma unroll
-      for (int e = 0; e < V; ++e) red[threadIdx.x * V + e] = p ? db[i][e] : dw[i][e];
+      sts<V>(red + threadIdx.x * V, p ? db[i] : dw[i]);
       __syncthreads();
       const int c = (i * LPR + lane) * V;
       if (rg == 0 && c < d)
@@ -369,7 +371,8 @@ __global__ void __launch_bounds__(NT) seq_stats_kernel(const Norm a, const Cols 
     const long long t0 = ((long long)q.tile * s.RL + q.rl) * s.run;
     const long long t1 = t0 + s.run < n ? t0 + s.run : n;
     if (t0 < t1) {
-      float k = 0.f, s1 = 0.f, s2 = 0.f;
+      float k = 0.f;
+      F2 p1 = both(0.f), p2 = both(0.f);
       for (long long t = t0; t < t1; t += 8) {
         Vec<TI, V> raw[8];
 #pragma unroll
@@ -377,14 +380,18 @@ __global__ void __launch_bounds__(NT) seq_stats_kernel(const Norm a, const Cols 
         if (t == t0) k = get(raw[0], 0);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (t + i < t1)
+          if (t + i < t1) {
+            Pairs<V> u;
+            to_pairs<V>(u, raw[i]);
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-              const float u = get(raw[i], e) - k;
-              s1 += u;
-              s2 = fmaf(u, u, s2);
+            for (int e = 0; e < (V + 1) / 2; ++e) {
+              const F2 q = add(u[e], both(-k));
+              p1 = add(p1, q);
+              p2 = fma(q, q, p2);
             }
+          }
       }
+      const float s1 = total<V>(p1), s2 = total<V>(p2);
       const float cnt = (float)((t1 - t0) * V), mean = s1 / cnt;
       mine = make_float3(cnt, k + mean, fmaxf(s2 - s1 * mean, 0.f));
     }
@@ -458,7 +465,7 @@ __global__ void __launch_bounds__(NT) seq_apply_kernel(const Norm a, const Cols 
   TO *y = static_cast<TO *>(a.y) + q.b * a.sy.b + q.h0 * a.sy.h + q.c;
   const float2 st = stats[(long long)q.b * a.H + h];
   const long long hc = (long long)q.h0 * a.d + q.c;
-  float w[V], bs[V];
+  Pairs<V> w, bs;
   affine_of<V>(w, bs, a, hc, true);
   const long long t0 = ((long long)q.tile * s.RL + q.rl) * s.run;
   const long long t1 = t0 + s.run < n ? t0 + s.run : n;
@@ -468,13 +475,14 @@ __global__ void __launch_bounds__(NT) seq_apply_kernel(const Norm a, const Cols 
     for (int i = 0; i < 4; ++i) raw[i] = load_if<TI, V>(x + (t + i) * a.sx.t, t + i < t1);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      Row<V> o;
+      Pairs<V> u;
+      to_pairs<V>(u, raw[i]);
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float p = fmaf((get(raw[i], e) - st.x) * st.y, w[e], bs[e]);
-        put(o, e, a.silu ? silu(p) : p);
+      for (int e = 0; e < (V + 1) / 2; ++e) {
+        u[e] = fma(mul(add(u[e], both(-st.x)), both(st.y)), w[e], bs[e]);
+        if (a.silu) u[e] = silu(u[e]);
       }
-      if (t + i < t1) store(y + (t + i) * a.sy.t, o);
+      if (t + i < t1) store_pairs<TO, V>(y + (t + i) * a.sy.t, u);
     }
   }
 }
@@ -482,19 +490,19 @@ __global__ void __launch_bounds__(NT) seq_apply_kernel(const Norm a, const Cols 
 // Per channel the sums of dy act'(p) xh and dy act'(p) over a row tile: [b, tile][2][h, c].
 template <typename TI, typename TO, int V>
 __global__ void __launch_bounds__(NT) seq_sums_kernel(const Norm a, const Cols s, float *part) {
-  __shared__ float red[NT * V];
+  __shared__ __align__(16) float red[NT * V];
   const At q = at_of(a, s, V);
   const int n = tokens_of(a.lengths, q.b, a.T);
-  float dw[V], db[V];
+  Pairs<V> dw, db;
 #pragma unroll
-  for (int e = 0; e < V; ++e) dw[e] = db[e] = 0.f;
+  for (int e = 0; e < (V + 1) / 2; ++e) dw[e] = db[e] = both(0.f);
   const long long hc = (long long)q.h0 * a.d + q.c;
   if (q.mine) {
     const int h = q.h0 + q.c / a.d;
     const TI *x = static_cast<const TI *>(a.x) + q.b * a.sx.b + q.h0 * a.sx.h + q.c;
     const TO *dy = static_cast<const TO *>(a.dy) + q.b * a.sdy.b + q.h0 * a.sdy.h + q.c;
     const float2 st = reinterpret_cast<const float2 *>(a.stats)[(long long)q.b * a.H + h];
-    float w[V], bs[V];
+    Pairs<V> w, bs;
     affine_of<V>(w, bs, a, hc, true);
     const long long t0 = ((long long)q.tile * s.RL + q.rl) * s.run;
     const long long t1 = t0 + s.run < n ? t0 + s.run : n;
@@ -507,24 +515,25 @@ __global__ void __launch_bounds__(NT) seq_sums_kernel(const Norm a, const Cols s
         yr[i] = load_if<TO, V>(dy + (t + i) * a.sdy.t, t + i < t1);
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 4; ++i) {
+        if (t + i >= t1) continue;
+        Pairs<V> xh, k;
+        to_pairs<V>(xh, xr[i]);
+        to_pairs<V>(k, yr[i]);
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float xh = (get(xr[i], e) - st.x) * st.y;
-          float k = get(yr[i], e);
-          if (a.silu) k *= act_grad(fmaf(xh, w[e], bs[e]));
-          if (t + i < t1) {
-            db[e] += k;
-            dw[e] = fmaf(k, xh, dw[e]);
-          }
+        for (int e = 0; e < (V + 1) / 2; ++e) {
+          xh[e] = mul(add(xh[e], both(-st.x)), both(st.y));
+          if (a.silu) k[e] = mul(k[e], silu_grad(fma(xh[e], w[e], bs[e])));
+          db[e] = add(db[e], k[e]);
+          dw[e] = fma(k[e], xh[e], dw[e]);
         }
+      }
     }
   }
   float *out = part + ((long long)q.b * s.tiles + q.tile) * 2 * a.H * a.d + hc;
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
-#pragma unroll
-    for (int e = 0; e < V; ++e) red[threadIdx.x * V + e] = p ? db[e] : dw[e];
+    sts<V>(red + threadIdx.x * V, p ? db : dw);
     __syncthreads();
     if (q.rl == 0 && q.mine)
 #pragma unroll
@@ -602,7 +611,7 @@ __global__ void __launch_bounds__(NT) seq_grad_kernel(const Norm a, const Cols s
   const float2 st = reinterpret_cast<const float2 *>(a.stats)[(long long)q.b * a.H + h];
   const float2 mk = means[(long long)q.b * a.H + h];
   const long long hc = (long long)q.h0 * a.d + q.c;
-  float w[V], bs[V];
+  Pairs<V> w, bs;
   affine_of<V>(w, bs, a, hc, true);
   const long long t0 = ((long long)q.tile * s.RL + q.rl) * s.run;
   const long long t1 = t0 + s.run < a.T ? t0 + s.run : a.T;
@@ -617,15 +626,17 @@ __global__ void __launch_bounds__(NT) seq_grad_kernel(const Norm a, const Cols s
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      Row<V> o;
+      Pairs<V> xh, k;
+      to_pairs<V>(xh, xr[i]);
+      to_pairs<V>(k, yr[i]);
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float xh = (get(xr[i], e) - st.x) * st.y;
-        float k = get(yr[i], e);
-        if (a.silu) k *= act_grad(fmaf(xh, w[e], bs[e]));
-        put(o, e, t + i < n ? st.y * (fmaf(k, w[e], -mk.x) - xh * mk.y) : 0.f);
+      for (int e = 0; e < (V + 1) / 2; ++e) {
+        xh[e] = mul(add(xh[e], both(-st.x)), both(st.y));
+        if (a.silu) k[e] = mul(k[e], silu_grad(fma(xh[e], w[e], bs[e])));
+        k[e] = mul(both(st.y), fma(xh[e], both(-mk.y), fma(k[e], w[e], both(-mk.x))));
+        k[e] = keep_if(k[e], t + i < n);
       }
-      if (t + i < t1) store(dx + (t + i) * a.sdx.t, o);
+      if (t + i < t1) store_pairs<TI, V>(dx + (t + i) * a.sdx.t, k);
     }
   }
 }
@@ -689,7 +700,9 @@ cudaError_t forward(const Norm &a, cudaStream_t st) {
       if (a.d <= 16 * V) return go(token_kernel<TI, TO, V, 16, 1, 4>, 16, 4);
       if (a.d <= 32 * V) return go(token_kernel<TI, TO, V, 32, 1, 4>, 32, 4);
       if (a.d <= 64 * V) return go(token_kernel<TI, TO, V, 32, 2, 2>, 32, 2);
-      if (a.d <= 128 * V) return go(token_kernel<TI, TO, V, 32, 4, 1>, 32, 1);
+      if (a.d <= 128 * V) return go(token_kernel<TI, TO, V, 128, 1, 2>, 128, 2);
+      if (a.d <= 256 * V) return go(token_kernel<TI, TO, V, 256, 1, 2>, 256, 2);
+      if (a.d <= 1024 * V) return go(token_kernel<TI, TO, V, 256, 4, 1>, 256, 1);
     }
     if (a.d <= 32) return go(token_kernel<TI, TO, 1, 32, 1, 4>, 32, 4);
     if (a.d <= 256) return go(token_kernel<TI, TO, 1, 32, 8, 1>, 32, 1);
@@ -738,8 +751,10 @@ cudaError_t backward(const Norm &a, cudaStream_t st) {
       if (a.d <= 8 * V) return go(token_backward_kernel<TI, TO, V, 8, 1, 2>, V);
       if (a.d <= 16 * V) return go(token_backward_kernel<TI, TO, V, 16, 1, 2>, V);
       if (a.d <= 32 * V) return go(token_backward_kernel<TI, TO, V, 32, 1, 2>, V);
-      if (a.d <= 64 * V) return go(token_backward_kernel<TI, TO, V, 32, 2, 1>, V);
-      if (V == 4 && a.d <= 128 * V) return go(token_backward_kernel<TI, TO, V, 32, 4, 1>, V);
+      if (a.d <= 64 * V) return go(token_backward_kernel<TI, TO, V, 64, 1, 2>, V);
+      if (a.d <= 128 * V) return go(token_backward_kernel<TI, TO, V, 128, 1, 2>, V);
+      if (a.d <= 256 * V) return go(token_backward_kernel<TI, TO, V, 256, 1, 2>, V);
+      if (a.d <= 512 * V) return go(token_backward_kernel<TI, TO, V, 256, 2, 1>, V);
     }
     if (a.d <= 32) return go(token_backward_kernel<TI, TO, 1, 32, 1, 2>, 1);
     if (a.d <= 256) return go(token_backward_kernel<TI, TO, 1, 32, 8, 1>, 1);

@@ -651,9 +651,7 @@ __global__ void __launch_bounds__(32 * W, 12 / W) grad_kernel(const Scan a, cons
           values<T, V>(r, raw + 3 * TS * CB + at);
 #pragma unroll
           for (int j = 0; j < P; ++j) {
-            const F2 s = sigmoid(kk[j]), one = both(1.f);
-            const F2 ds = mul(s, fma(kk[j], add(one, mul(s, both(-1.f))), one));
-            r[j] = keep_if(mul(mul(r[j], ds), fma(D[j], x[j], yv[j])), live);
+            r[j] = keep_if(mul(mul(r[j], silu_grad(kk[j])), fma(D[j], x[j], yv[j])), live);
           }
           store_pairs<T, V>(dzp + (t0 + t) * a.sdz.t + kc, r);
         }
