@@ -22,17 +22,25 @@ using bf16 = __nv_bfloat16;
 // Channels of one (batch, head) in vectors of V, `nv` of them, walked in
 // blocks of `nvb` vectors by `RL` row groups side by side.
 struct Split {
-  int nv, nvb, cb, RL, tiles;        // vectors, vectors a block, blocks of channels, row groups, row tiles
+  int nv, nvb, cb, RL, tiles, run;   // vectors, vectors a block, blocks of channels, row groups, row tiles, rows of a run
 };
-Split split_of(int d, int V, int T, int rows, int widest, int threads) {
+// Runs as long as they can be while the grid still fills the GPU's `slots`
+// CTAs, in one wave: long runs amortise the taps, the halo rows and the partial
+// sums. At least `least` rows, a multiple of `batch`.
+Split split_of(long long units, int d, int V, int T, int batch, int least, int widest, int threads, int slots) {
   Split s;
   s.nv = d / V;
   s.nvb = s.nv < widest ? s.nv : widest;
   s.cb = (s.nv + s.nvb - 1) / s.nvb;
   s.RL = threads / s.nvb;
-  const long long need = ((long long)T + rows - 1) / rows;
-  if (s.RL > need) s.RL = (int)need;
-  s.tiles = (int)(((long long)T + (long long)rows * s.RL - 1) / ((long long)rows * s.RL));
+  const long long most = ((long long)T + least - 1) / least;
+  if (s.RL > most) s.RL = (int)most;
+  long long tiles = slots / (units * s.cb);
+  if (tiles < 1) tiles = 1;
+  long long run = ((long long)T + tiles * s.RL - 1) / (tiles * s.RL);
+  run = run < least ? least : run;
+  s.run = (int)((run + batch - 1) / batch * batch);
+  s.tiles = (int)(((long long)T + (long long)s.run * s.RL - 1) / ((long long)s.run * s.RL));
   return s;
 }
 
@@ -72,11 +80,16 @@ __device__ __forceinline__ void taps_of(Pairs<V> (&f)[MAXW], Pairs<V> &bias, con
   }
 }
 
-// A thread walks `run` rows in batches of RB, the next batch's loads issued
-// before the current one is computed; the w - 1 rows before a batch stay in
-// registers, and the taps are read once for the whole run.
+// A thread walks `run` rows in batches of RB. Its rows come into its own slots
+// of shared memory by asynchronous copies, two batches ahead (64 KB on the way
+// per SM for V = 4 bf16 channels), so it waits for its copies and for no
+// barrier; the w - 1 rows before a batch stay in registers, and the taps are
+// read once for the whole run.
+constexpr int AHEAD = 3;             // batches of shared-memory slots
 template <typename T, int V, int MAXW, bool EXACT, int RB>
-__global__ void __launch_bounds__(NT, 2) conv_kernel(const Conv a, const Split sp, const int run) {
+__global__ void __launch_bounds__(NT, 2) conv_kernel(const Conv a, const Split sp) {
+  extern __shared__ __align__(16) unsigned char slots[];   // [AHEAD][RB][threads][V]
+  const int run = sp.run;
   unsigned blk = blockIdx.x;
   const int tile = blk % sp.tiles;
   blk /= sp.tiles;
@@ -101,24 +114,33 @@ __global__ void __launch_bounds__(NT, 2) conv_kernel(const Conv a, const Split s
   if (t0 >= n) return;
 
   constexpr int P = (V + 1) / 2;
-  Vec<T, V> next[RB];
+  const T *xp = x + t0 * a.sx.t;                // the next batch to copy
+  T *slot = reinterpret_cast<T *>(slots) + threadIdx.x * V;
+  const int pitch = blockDim.x * V;
+  auto fetch = [&](auto whole, int left, int buf) {
+#pragma unroll
+    for (int i = 0; i < RB; ++i) copy_in<T, V>(slot + (buf * RB + i) * pitch, xp + i * a.sx.t, whole || i < left);
+    copies_sent();
+    xp += RB * a.sx.t;
+  };
+  int left = (int)(t1 - t0);
+#pragma unroll
+  for (int k = 0; k < AHEAD - 1; ++k) fetch(std::false_type{}, left - k * RB, k);
   Pairs<V> win[RB + MAXW - 1];                  // rows tb - (MAXW - 1) .. tb + RB - 1
 #pragma unroll
   for (int i = 0; i < MAXW - 1; ++i)
     to_pairs<V>(win[i], row_of<T, V>(x, a.sx.t, hist, w, d, t0 - (MAXW - 1) + i, EXACT || i + w >= MAXW));
-  const T *xp = x + t0 * a.sx.t;
-#pragma unroll
-  for (int i = 0; i < RB; ++i) next[i] = load_if<T, V>(xp + i * a.sx.t, t0 + i < t1);
   Pairs<V> f[MAXW], bias;
   taps_of<V, MAXW>(f, bias, a, (long long)h * d + c, true);
   T *y = static_cast<T *>(a.y) + b * a.sy.b + h * a.sy.h + c + t0 * a.sy.t;
-  // whole: every row of this batch, and of the next one that is fetched, is live
+  int buf = 0;
+  // whole: every row of this batch, and of the one that is fetched, is live
   auto batch = [&](auto whole, int left) {
+    fetch(whole, left - (AHEAD - 1) * RB, buf == 0 ? AHEAD - 1 : buf - 1);
+    copies_done<AHEAD - 1>();
 #pragma unroll
-    for (int i = 0; i < RB; ++i) to_pairs<V>(win[MAXW - 1 + i], next[i]);
-    xp += RB * a.sx.t;
-#pragma unroll
-    for (int i = 0; i < RB; ++i) next[i] = load_if<T, V>(xp + i * a.sx.t, whole || RB + i < left);
+    for (int i = 0; i < RB; ++i) values<T, V>(win[MAXW - 1 + i], slot + (buf * RB + i) * pitch);
+    buf = buf == AHEAD - 1 ? 0 : buf + 1;
 #pragma unroll
     for (int r = 0; r < RB; ++r) {
       Pairs<V> p;
@@ -138,9 +160,9 @@ __global__ void __launch_bounds__(NT, 2) conv_kernel(const Conv a, const Split s
 #pragma unroll
       for (int e = 0; e < P; ++e) win[i][e] = win[RB + i][e];
   };
-  int left = (int)(t1 - t0);
-  for (; left >= 2 * RB; left -= RB) batch(std::true_type{}, left);
+  for (; left >= AHEAD * RB; left -= RB) batch(std::true_type{}, left);
   for (; left > 0; left -= RB) batch(std::false_type{}, left);
+  copies_done();
 }
 
 // Gradients. A thread walks RB rows at a time through a run of `run` rows: it
@@ -151,7 +173,8 @@ __global__ void __launch_bounds__(NT, 2) conv_kernel(const Conv a, const Split s
 // partial, which a second launch sums in a fixed order (no atomics: the same
 // inputs give the same bits).
 template <typename T, int V, int MAXW, bool EXACT, int RB>
-__global__ void __launch_bounds__(BT, 3) conv_backward_kernel(const Conv a, const Split sp, const int run, float *part) {
+__global__ void __launch_bounds__(BT, 3) conv_backward_kernel(const Conv a, const Split sp, float *part) {
+  const int run = sp.run;
   extern __shared__ __align__(16) float red[];               // [threads][V]
   unsigned blk = blockIdx.x;
   const int tile = blk % sp.tiles;
@@ -360,20 +383,8 @@ __global__ void __launch_bounds__(NT) conv_step_kernel(const Conv a, const long 
     if (j < w - 1) store(hist + (long long)(w - 2 - j) * d, raw[j]);
 }
 
-// Rows a thread walks in the backward: long runs amortise the 2 (w - 1) rows
-// that neighbours also read and the partial sums; short ones give small
-// problems enough threads.
-struct BackPlan {
-  int run;
-  Split sp;
-};
-BackPlan backward_plan(int B, int H, int T, int d, int V) {
-  BackPlan p;
-  p.run = 128;
-  const long long lanes = (long long)B * H * (d / V);
-  while (p.run > 16 && lanes * ((T + p.run - 1) / p.run) < (long long)kSMs * 768) p.run /= 2;
-  p.sp = split_of(d, V, T, p.run, 32, BT);
-  return p;
+Split backward_split(int B, int H, int T, int d, int V) {
+  return split_of((long long)B * H, d, V, T, 4, 16, 32, BT, kSMs * 3);
 }
 
 void collapse(Conv &c, std::initializer_list<Str *> ss) {
@@ -399,14 +410,16 @@ cudaError_t conv_launch(Conv c, cudaStream_t st) {
            fits(c.tail, {}, c.d, V, el);
   };
   auto go = [&](auto kern, int V, int rows) {
-    // long runs amortise the taps and the halo rows; short ones give small
-    // problems enough threads
-    int run = 64;
-    while (run > rows && (long long)c.B * c.H * (c.d / V) * ((c.T + run - 1) / run) < (long long)kSMs * 768) run /= 2;
-    const Split sp = split_of(c.d, V, c.T, run, 64, NT);
+    const Split sp = split_of((long long)c.B * c.H, c.d, V, c.T, rows, rows, 64, NT, kSMs * 2);
     const long long grid = (long long)sp.tiles * sp.cb * c.B * c.H;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-    kern<<<(unsigned)grid, sp.nvb * sp.RL, 0, st>>>(c, sp, run);
+    const int threads = sp.nvb * sp.RL;
+    const size_t smem = (size_t)AHEAD * rows * threads * V * el;
+    if (smem > 48 * 1024) {
+      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (e != cudaSuccess) return e;
+    }
+    kern<<<(unsigned)grid, threads, smem, st>>>(c, sp);
     return cudaGetLastError();
   };
   auto pick = [&](auto t, auto v) {
@@ -428,8 +441,8 @@ size_t conv_backward_ws(int B, int H, int T, int d, int w) {
   for (const int V : {1, 2, 4})
     for (const bool joined : {false, true}) {
       if ((joined ? H * d : d) % V) continue;
-      const BackPlan p = joined ? backward_plan(B, 1, T, H * d, V) : backward_plan(B, H, T, d, V);
-      if ((size_t)p.sp.tiles > tiles) tiles = p.sp.tiles;
+      const Split p = joined ? backward_split(B, 1, T, H * d, V) : backward_split(B, H, T, d, V);
+      if ((size_t)p.tiles > tiles) tiles = p.tiles;
     }
   return up256((size_t)B * tiles * H * d * (w + 1) * 4);
 }
@@ -443,12 +456,11 @@ cudaError_t conv_backward_launch(Conv c, cudaStream_t st) {
   };
   float *part = static_cast<float *>(c.ws);
   auto go = [&](auto kern, int V) {
-    const BackPlan pl = backward_plan(c.B, c.H, c.T, c.d, V);
-    const Split &sp = pl.sp;
+    const Split sp = backward_split(c.B, c.H, c.T, c.d, V);
     const long long grid = (long long)sp.tiles * sp.cb * c.B * c.H;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
     const int threads = sp.nvb * sp.RL;
-    kern<<<(unsigned)grid, threads, threads * V * sizeof(float), st>>>(c, sp, pl.run, part);
+    kern<<<(unsigned)grid, threads, threads * V * sizeof(float), st>>>(c, sp, part);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const long long ch = (long long)c.H * c.d, n = ch * (c.w + 1);

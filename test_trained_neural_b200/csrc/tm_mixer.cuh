@@ -143,7 +143,8 @@ __device__ __forceinline__ void copy_in(T *dst, const T *src, bool live) {
   }
 }
 __device__ __forceinline__ void copies_sent() { asm volatile("cp.async.commit_group;"); }
-__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+template <int LEFT = 0>
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
 
 // Two fp32 values in one 64-bit register: one instruction for both.
 struct F2 {

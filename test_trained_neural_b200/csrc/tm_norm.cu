@@ -18,6 +18,7 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 constexpr int NT = 256;
+constexpr int GT = 128;              // threads of a token-wise gradient CTA (more where a row takes more)
 
 // Sum over groups of LPR threads. Groups wider than a warp go through `red`
 // (NT / 32 floats) and a barrier: every thread of the CTA calls it, and the next
@@ -158,10 +159,11 @@ __global__ void __launch_bounds__(NT) token_wide_kernel(const Norm a) {
 // NT / LPR; the lane's channels are fixed, so the parameters' gradients are
 // summed in registers over all rows of the CTA.
 template <typename TI, typename TO, int V, int LPR, int IT, int RPT>
-__global__ void __launch_bounds__(NT) token_backward_kernel(const Norm a, const int tiles, float *part) {
-  extern __shared__ __align__(16) float red[];          // [NT][V]
-  __shared__ float sums[2][NT / 32];
-  constexpr int ROWS = NT / LPR, P = (V + 1) / 2;
+__global__ void __launch_bounds__(LPR > GT ? LPR : GT) token_backward_kernel(const Norm a, const int tiles, float *part) {
+  extern __shared__ __align__(16) float red[];          // [threads][V]
+  constexpr int CTA = LPR > GT ? LPR : GT;
+  __shared__ float sums[2][CTA / 32];
+  constexpr int ROWS = CTA / LPR, P = (V + 1) / 2;
   const int tile = blockIdx.x % tiles, bh = blockIdx.x / tiles;
   const int h = bh % a.H, b = bh / a.H, d = a.d;
   const int lane = threadIdx.x % LPR, rg = threadIdx.x / LPR;
@@ -415,17 +417,11 @@ __global__ void __launch_bounds__(NT) seq_stats_kernel(const Norm a, const Cols 
 // Joins the partials of one (batch, head), in 64 bits, in a fixed order.
 __global__ void __launch_bounds__(NT) seq_join_kernel(const Norm a, const Cols s, const int V, const float2 *part,
                                                       float2 *stats) {
-  __shared__ double red[3][NT / 32];
+  __shared__ double red[2][NT / 32];
   const int bh = blockIdx.x, h = bh % a.H, b = bh / a.H;
   const int n = tokens_of(a.lengths, b, a.T);
-  const int vh = a.d / V;
-  const long long vecs = (long long)a.H * vh, total = (long long)s.tiles * vh;
-  const long long span = (long long)s.run * s.RL;
-  auto count = [&](long long i) {
-    const long long left = n - (i / vh) * span;
-    return (double)((left < 0 ? 0 : left < span ? left : span) * V);
-  };
-  auto entry = [&](long long i) { return part[((long long)b * s.tiles + i / vh) * vecs + (long long)h * vh + i % vh]; };
+  const int vh = a.d / V, vecs = a.H * vh;
+  const int span = s.run * s.RL;
   auto all = [&](double x, int k) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
@@ -436,23 +432,27 @@ __global__ void __launch_bounds__(NT) seq_join_kernel(const Norm a, const Cols s
     for (int i = 0; i < NT / 32; ++i) y += red[k][i];
     return y;
   };
-  const double cnt = (double)n * a.d;
+  // sum of squares = sum over the parts of (theirs about their mean + count mean^2); 64 bits leave the
+  // variance exact to 1e-10 beside a mean a thousand times the spread
   double s1 = 0., s2 = 0.;
-  for (long long i = threadIdx.x; i < total; i += NT) {
-    const double k = count(i);
-    if (k > 0.) s1 += k * entry(i).x;
-  }
-  const double mean = cnt > 0. ? all(s1, 0) / cnt : 0.;
-  for (long long i = threadIdx.x; i < total; i += NT) {
-    const double k = count(i);
-    if (k > 0.) {
-      const float2 e = entry(i);
-      s2 += e.y + k * (e.x - mean) * (e.x - mean);
+  for (int t = threadIdx.x / 32; t < s.tiles; t += NT / 32) {
+    const long long left = n - (long long)t * span;
+    if (left <= 0) break;
+    const double k = (double)(left < span ? left : span) * V;
+    const float2 *row = part + ((long long)b * s.tiles + t) * vecs + h * vh;
+    for (int i = threadIdx.x % 32; i < vh; i += 32) {
+      const float2 e = row[i];
+      s1 += k * e.x;
+      s2 += e.y + k * e.x * e.x;
     }
   }
+  const double cnt = (double)n * a.d;
+  s1 = all(s1, 0);
   s2 = all(s2, 1);
-  if (threadIdx.x == 0)
-    stats[bh] = n > 0 ? make_float2((float)mean, (float)(1. / sqrt(s2 / cnt + (double)a.eps))) : make_float2(0.f, 0.f);
+  if (threadIdx.x == 0) {
+    const double mean = n > 0 ? s1 / cnt : 0., var = n > 0 ? fmax(s2 / cnt - mean * mean, 0.) : 0.;
+    stats[bh] = n > 0 ? make_float2((float)mean, (float)(1. / sqrt(var + (double)a.eps))) : make_float2(0.f, 0.f);
+  }
 }
 
 template <typename TI, typename TO, int V>
@@ -668,15 +668,17 @@ cudaError_t pair_sum(const float *part, int parts, long long hd, float *dweight,
   return cudaGetLastError();
 }
 
-// CTAs of a (batch, head) that share its rows in the token-wise backward:
-// enough to fill the GPU a few times over, each with rows to sum over.
-int token_tiles(int B, int H, int T, int d) {
+// CTAs of a (batch, head) that share its rows token by token: together one wave
+// of `slots` CTAs, each with rows to walk.
+int token_tiles(int B, int H, int T, int slots, int rows) {
   const long long bh = (long long)B * H;
-  long long tiles = ((long long)kSMs * 8 + bh - 1) / bh;
-  const long long most = ((long long)T + 31) / 32;
+  long long tiles = slots / bh;
+  const long long most = ((long long)T + rows - 1) / rows;
   if (tiles > most) tiles = most;
   return (int)(tiles < 1 ? 1 : tiles);
 }
+// in the gradient: 4 CTAs of 128 threads an SM, 2 of 256 for wide rows (the partials' count is this)
+int gradient_tiles(int B, int H, int T, int d) { return token_tiles(B, H, T, kSMs * (d > 512 ? 2 : 4), 16); }
 
 bool affine_fits(const Norm &a) {
   return reinterpret_cast<uintptr_t>(a.weight) % 16 == 0 && reinterpret_cast<uintptr_t>(a.bias) % 16 == 0;
@@ -740,10 +742,10 @@ cudaError_t backward(const Norm &a, cudaStream_t st) {
   const long long bh = (long long)a.B * a.H, hd = (long long)a.H * a.d;
   float *part = static_cast<float *>(a.ws);
   if (a.over == kToken) {
-    const int tiles = token_tiles(a.B, a.H, a.T, a.d);
+    const int tiles = gradient_tiles(a.B, a.H, a.T, a.d);
     if (bh * tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
-    auto go = [&](auto kern, int VV) {
-      kern<<<(unsigned)(bh * tiles), NT, NT * VV * sizeof(float), st>>>(a, tiles, part);
+    auto go = [&](auto kern, int VV, int threads = GT) {
+      kern<<<(unsigned)(bh * tiles), threads, threads * VV * sizeof(float), st>>>(a, tiles, part);
       const cudaError_t e = cudaGetLastError();
       return e != cudaSuccess ? e : pair_sum(part, a.B * tiles, hd, a.dweight, a.dbias, st);
     };
@@ -753,8 +755,8 @@ cudaError_t backward(const Norm &a, cudaStream_t st) {
       if (a.d <= 32 * V) return go(token_backward_kernel<TI, TO, V, 32, 1, 2>, V);
       if (a.d <= 64 * V) return go(token_backward_kernel<TI, TO, V, 64, 1, 2>, V);
       if (a.d <= 128 * V) return go(token_backward_kernel<TI, TO, V, 128, 1, 2>, V);
-      if (a.d <= 256 * V) return go(token_backward_kernel<TI, TO, V, 256, 1, 2>, V);
-      if (a.d <= 512 * V) return go(token_backward_kernel<TI, TO, V, 256, 2, 1>, V);
+      if (a.d <= 256 * V) return go(token_backward_kernel<TI, TO, V, 256, 1, 2>, V, 256);
+      if (a.d <= 512 * V) return go(token_backward_kernel<TI, TO, V, 256, 2, 1>, V, 256);
     }
     if (a.d <= 32) return go(token_backward_kernel<TI, TO, 1, 32, 1, 2>, 1);
     if (a.d <= 256) return go(token_backward_kernel<TI, TO, 1, 32, 8, 1>, 1);
@@ -801,7 +803,7 @@ size_t norm_ws(int B, int H, int T, int d, Over over) {
 
 size_t norm_backward_ws(int B, int H, int T, int d, Over over) {
   const size_t hd = (size_t)H * d;
-  if (over == kToken) return up256((size_t)B * token_tiles(B, H, T, d) * 2 * hd * 4);
+  if (over == kToken) return up256((size_t)B * gradient_tiles(B, H, T, d) * 2 * hd * 4);
   size_t tiles = 0;
   for (const int V : {1, 4, 8})
     for (const bool joined : {false, true}) {
