@@ -68,62 +68,79 @@ __device__ __forceinline__ void affine_of(Pairs<V> &w, Pairs<V> &bs, const Norm 
 
 // ---- one token
 
-// CTA: one (batch, head), NT / LPR rows side by side, RPT rows each.
+// CTA: one (batch, head) and the rows tile, tile + tiles, ... in steps of
+// NT / LPR rows, RPT steps at a time; the next rows are on their way while these
+// are computed, and the parameters stay in registers.
 template <typename TI, typename TO, int V, int LPR, int IT, int RPT>
 __global__ void __launch_bounds__(NT) token_kernel(const Norm a, const int tiles) {
-  constexpr int P = (V + 1) / 2;
+  constexpr int P = (V + 1) / 2, ROWS = NT / LPR;
   __shared__ float red[2][NT / 32];
   const int tile = blockIdx.x % tiles, bh = blockIdx.x / tiles;
   const int h = bh % a.H, b = bh / a.H, d = a.d;
-  const int lane = threadIdx.x % LPR;
+  const int lane = threadIdx.x % LPR, rg = threadIdx.x / LPR;
   const int n = tokens_of(a.lengths, b, a.T);
-  const long long t0 = ((long long)tile * (NT / LPR) + threadIdx.x / LPR) * RPT;
-  const TI *x = static_cast<const TI *>(a.x) + b * a.sx.b + h * a.sx.h + t0 * a.sx.t + lane * V;
-  TO *y = static_cast<TO *>(a.y) + b * a.sy.b + h * a.sy.h + t0 * a.sy.t + lane * V;
-  Vec<TI, V> raw[RPT][IT];
+  const long long first = (long long)tile * ROWS * RPT + rg;
+  const TI *x = static_cast<const TI *>(a.x) + b * a.sx.b + h * a.sx.h + first * a.sx.t + lane * V;
+  TO *y = static_cast<TO *>(a.y) + b * a.sy.b + h * a.sy.h + first * a.sy.t + lane * V;
+  const long long step = (long long)tiles * ROWS * RPT;
+  Vec<TI, V> next[RPT][IT];
+  auto fetch = [&](long long t0) {
 #pragma unroll
-  for (int r = 0; r < RPT; ++r)
+    for (int r = 0; r < RPT; ++r)
 #pragma unroll
-    for (int i = 0; i < IT; ++i)
-      raw[r][i] = load_if<TI, V>(x + r * a.sx.t + i * LPR * V, (i * LPR + lane) * V < d && t0 + r < n);
+      for (int i = 0; i < IT; ++i)
+        next[r][i] = load_if<TI, V>(x + r * ROWS * a.sx.t + i * LPR * V, (i * LPR + lane) * V < d && t0 + r * ROWS < n);
+    x += step * a.sx.t;
+  };
+  fetch(first);
   Pairs<V> w[IT], bs[IT];
 #pragma unroll
   for (int i = 0; i < IT; ++i)
     affine_of<V>(w[i], bs[i], a, (long long)h * d + (i * LPR + lane) * V, (i * LPR + lane) * V < d);
   const float inv = 1.f / d;
+  for (long long tb = (long long)tile * ROWS * RPT; tb < n; tb += step) {
+    Vec<TI, V> raw[RPT][IT];
 #pragma unroll
-  for (int r = 0; r < RPT; ++r) {
-    Pairs<V> u[IT];
-    F2 s = both(0.f);
+    for (int r = 0; r < RPT; ++r)
 #pragma unroll
-    for (int i = 0; i < IT; ++i) {
-      to_pairs<V>(u[i], raw[r][i]);
+      for (int i = 0; i < IT; ++i) raw[r][i] = next[r][i];
+    fetch(tb + step + rg);
 #pragma unroll
-      for (int e = 0; e < P; ++e) s = add(s, u[i][e]);          // lanes past d hold zeros
-    }
-    const float m = lanes_sum<LPR>(total<V>(s), red[0]) * inv;
-    s = both(0.f);
+    for (int r = 0; r < RPT; ++r) {
+      Pairs<V> u[IT];
+      F2 s = both(0.f);
 #pragma unroll
-    for (int i = 0; i < IT; ++i)
+      for (int i = 0; i < IT; ++i) {
+        to_pairs<V>(u[i], raw[r][i]);
 #pragma unroll
-      for (int e = 0; e < P; ++e) {
-        u[i][e] = add(u[i][e], both(-m));
-        if ((i * LPR + lane) * V < d) s = fma(u[i][e], u[i][e], s);
+        for (int e = 0; e < P; ++e) s = add(s, u[i][e]);        // lanes past d hold zeros
       }
-    const float rs = rsqrtf(fmaf(lanes_sum<LPR>(total<V>(s), red[1]), inv, a.eps));
-    const long long t = t0 + r;
-    if (t >= n) continue;
+      const float m = lanes_sum<LPR>(total<V>(s), red[0]) * inv;
+      s = both(0.f);
 #pragma unroll
-    for (int i = 0; i < IT; ++i) {
-      if ((i * LPR + lane) * V >= d) continue;
+      for (int i = 0; i < IT; ++i)
 #pragma unroll
-      for (int e = 0; e < P; ++e) {
-        u[i][e] = fma(mul(u[i][e], both(rs)), w[i][e], bs[i][e]);
-        if (a.silu) u[i][e] = silu(u[i][e]);
+        for (int e = 0; e < P; ++e) {
+          u[i][e] = add(u[i][e], both(-m));
+          if ((i * LPR + lane) * V < d) s = fma(u[i][e], u[i][e], s);
+        }
+      const float rs = rsqrtf(fmaf(lanes_sum<LPR>(total<V>(s), red[1]), inv, a.eps));
+      const long long t = tb + r * ROWS + rg;
+      if (t < n) {
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+          if ((i * LPR + lane) * V >= d) continue;
+#pragma unroll
+          for (int e = 0; e < P; ++e) {
+            u[i][e] = fma(mul(u[i][e], both(rs)), w[i][e], bs[i][e]);
+            if (a.silu) u[i][e] = silu(u[i][e]);
+          }
+          store_pairs<TO, V>(y + r * ROWS * a.sy.t + i * LPR * V, u[i]);
+        }
+        if (a.stats && lane == 0) reinterpret_cast<float2 *>(a.stats)[(long long)bh * a.T + t] = make_float2(m, rs);
       }
-      store_pairs<TO, V>(y + r * a.sy.t + i * LPR * V, u[i]);
     }
-    if (a.stats && lane == 0) reinterpret_cast<float2 *>(a.stats)[(long long)bh * a.T + t] = make_float2(m, rs);
+    y += step * a.sy.t;
   }
 }
 
@@ -435,16 +452,16 @@ __global__ void __launch_bounds__(NT) seq_join_kernel(const Norm a, const Cols s
   // sum of squares = sum over the parts of (theirs about their mean + count mean^2); 64 bits leave the
   // variance exact to 1e-10 beside a mean a thousand times the spread
   double s1 = 0., s2 = 0.;
-  for (int t = threadIdx.x / 32; t < s.tiles; t += NT / 32) {
+  const unsigned entries = (unsigned)s.tiles * vh;
+#pragma unroll 4
+  for (unsigned i = threadIdx.x; i < entries; i += NT) {
+    const unsigned t = i / vh;
     const long long left = n - (long long)t * span;
-    if (left <= 0) break;
+    if (left <= 0) continue;                             // rows behind the end: nothing was written for them
     const double k = (double)(left < span ? left : span) * V;
-    const float2 *row = part + ((long long)b * s.tiles + t) * vecs + h * vh;
-    for (int i = threadIdx.x % 32; i < vh; i += 32) {
-      const float2 e = row[i];
-      s1 += k * e.x;
-      s2 += e.y + k * e.x * e.x;
-    }
+    const float2 e = part[((long long)b * s.tiles + t) * vecs + h * vh + (i - t * vh)];
+    s1 += k * e.x;
+    s2 += e.y + k * e.x * e.x;
   }
   const double cnt = (double)n * a.d;
   s1 = all(s1, 0);
@@ -692,21 +709,21 @@ cudaError_t forward(const Norm &a, cudaStream_t st) {
   const long long bh = (long long)a.B * a.H;
   if (a.over == kToken) {
     auto go = [&](auto kern, int LPR, int RPT) {
-      const long long rows = (long long)NT / LPR * RPT, tiles = (a.T + rows - 1) / rows;
+      const int tiles = token_tiles(a.B, a.H, a.T, kSMs * 4, NT / LPR * RPT);
       if (bh * tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
-      kern<<<(unsigned)(bh * tiles), NT, 0, st>>>(a, (int)tiles);
+      kern<<<(unsigned)(bh * tiles), NT, 0, st>>>(a, tiles);
       return cudaGetLastError();
     };
     if (vec) {
-      if (a.d <= 8 * V) return go(token_kernel<TI, TO, V, 8, 1, 4>, 8, 4);
-      if (a.d <= 16 * V) return go(token_kernel<TI, TO, V, 16, 1, 4>, 16, 4);
-      if (a.d <= 32 * V) return go(token_kernel<TI, TO, V, 32, 1, 4>, 32, 4);
-      if (a.d <= 64 * V) return go(token_kernel<TI, TO, V, 32, 2, 2>, 32, 2);
+      if (a.d <= 8 * V) return go(token_kernel<TI, TO, V, 8, 1, 2>, 8, 2);
+      if (a.d <= 16 * V) return go(token_kernel<TI, TO, V, 16, 1, 2>, 16, 2);
+      if (a.d <= 32 * V) return go(token_kernel<TI, TO, V, 32, 1, 2>, 32, 2);
+      if (a.d <= 64 * V) return go(token_kernel<TI, TO, V, 64, 1, 2>, 64, 2);
       if (a.d <= 128 * V) return go(token_kernel<TI, TO, V, 128, 1, 2>, 128, 2);
       if (a.d <= 256 * V) return go(token_kernel<TI, TO, V, 256, 1, 2>, 256, 2);
       if (a.d <= 1024 * V) return go(token_kernel<TI, TO, V, 256, 4, 1>, 256, 1);
     }
-    if (a.d <= 32) return go(token_kernel<TI, TO, 1, 32, 1, 4>, 32, 4);
+    if (a.d <= 32) return go(token_kernel<TI, TO, 1, 32, 1, 2>, 32, 2);
     if (a.d <= 256) return go(token_kernel<TI, TO, 1, 32, 8, 1>, 32, 1);
     if (bh * a.T > 0x7fffffffLL) return cudaErrorInvalidValue;
     token_wide_kernel<TI, TO><<<(unsigned)(bh * a.T), NT, 0, st>>>(a);

@@ -143,22 +143,9 @@ __global__ void __launch_bounds__(32 * W, (NL >= 16 ? 8 : 16) / W) scan_kernel(c
       for (int s = 0; s < SPL; ++s) {
         const bool live = in && n0 + s < N;
         Af[c][s] = live ? a.A[(ch0 + c0 + c) * N + n0 + s] * kLog2e : 0.f;
-        hf[c][s] = live && a.state0 && (!LOCAL || seg == 0) ? a.state0[(chan + c) * N + n0 + s] : 0.f;
+        hf[c][s] = live && a.state0 && seg == 0 ? a.state0[(chan + c) * N + n0 + s] : 0.f;
       }
-    }
-    if (!LOCAL && seg > 0) {
-      // join the segments before this one: what each adds from a zero state,
-      // and its decay exp(A sum e); segment 0's holds the initial state
-      for (int q = 0; q < seg; ++q)
-#pragma unroll
-        for (int c = 0; c < CPL; ++c) {
-          if (c_blk + c0 + c >= a.d) continue;
-          const float es = esum[q * per + chan + c];
-          float l[SPL];
-          lds<SPL>(l, hloc + (q * per + chan + c) * NP + n0);
-#pragma unroll
-          for (int s = 0; s < SPL; ++s) hf[c][s] = q == 0 ? l[s] : fmaf(ex2(Af[c][s] * es), hf[c][s], l[s]);
-        }
+      if (!LOCAL && seg > 0 && in) lds<SPL>(hf[c], hloc + ((seg - 1) * per + chan + c) * NP + n0);
     }
 #pragma unroll
     for (int c = 0; c < C2; ++c)
@@ -332,7 +319,8 @@ cudaError_t run(const Scan &c, const Plan &p, cudaStream_t st) {
   float *esum = hloc + (size_t)(p.S - 1) * c.B * c.H * c.d * NL * SPL;
   if (p.S > 1) {
     local<<<(unsigned)(units * (p.S - 1)), 32 * W, smem, st>>>(c, p, hloc, esum);
-    const cudaError_t e = cudaGetLastError();
+    cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess && p.S > 2) e = join_segments(c, p.S, p.S - 2, NL * SPL, hloc, nullptr, esum, st);
     if (e != cudaSuccess) return e;
   }
   whole<<<(unsigned)(units * p.S), 32 * W, smem, st>>>(c, p, hloc, esum);

@@ -451,24 +451,8 @@ __global__ void __launch_bounds__(32 * W, 12 / W) grad_kernel(const Scan a, cons
         hf[c][s] = 0.f;
       }
       if (!SPLIT || c_blk + c0 + c >= a.d) continue;
-#pragma unroll 4
-      for (int q = 0; q < w.seg; ++q) {
-        const long long at = q * per + chan + c;
-        const float es = ws[pl.esum + at];
-        float l[SPL];
-        lds<SPL>(l, ws + pl.hloc + at * NP + n0);
-#pragma unroll
-        for (int s = 0; s < SPL; ++s) hf[c][s] = q == 0 ? l[s] : fmaf(ex2(Af[c][s] * es), hf[c][s], l[s]);
-      }
-#pragma unroll 4
-      for (int q = pl.S - 1; q > w.seg; --q) {
-        const long long at = q * per + chan + c;
-        const float es = ws[pl.esum + at];
-        float l[SPL];
-        lds<SPL>(l, ws + pl.gloc + at * NP + n0);
-#pragma unroll
-        for (int s = 0; s < SPL; ++s) Rf[c][s] = fmaf(ex2(Af[c][s] * es), Rf[c][s], l[s]);
-      }
+      if (w.seg > 0) lds<SPL>(hf[c], ws + pl.hloc + ((w.seg - 1) * per + chan + c) * NP + n0);
+      if (w.seg < pl.S - 1) lds<SPL>(Rf[c], ws + pl.gloc + ((w.seg + 1) * per + chan + c) * NP + n0);
     }
 #pragma unroll
     for (int s = 0; s < SPL; ++s) {
@@ -797,6 +781,8 @@ cudaError_t run(const Scan &c, const Plan &p, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   states<<<(unsigned)grid, thr, sm1, st>>>(c, p, ws);
   e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  if (SPLIT) e = join_segments(c, p.S, p.S - 1, NP, ws + p.hloc, ws + p.gloc, ws + p.esum, st);
   if (e != cudaSuccess) return e;
   constexpr size_t sm2 = GradSmem<T, NL, VB, W>::bytes;
   auto grad = grad_kernel<T, NL, VB, W, SPLIT>;
