@@ -430,8 +430,11 @@ cudaError_t conv_launch(Conv c, cudaStream_t st) {
     return go(conv_kernel<T, V, 8, false, 4>, V, 4);
   };
   using std::integral_constant;
-  if (c.bf16) return vec(4) ? pick(bf16(), integral_constant<int, 4>()) : pick(bf16(), integral_constant<int, 1>());
-  return vec(4) ? pick(0.f, integral_constant<int, 4>()) : pick(0.f, integral_constant<int, 1>());
+  auto widest = [&](auto t) {
+    if (vec(4)) return pick(t, integral_constant<int, 4>());
+    return vec(2) ? pick(t, integral_constant<int, 2>()) : pick(t, integral_constant<int, 1>());
+  };
+  return c.bf16 ? widest(bf16()) : widest(0.f);
 }
 
 // The partials of conv_backward_kernel: the largest over the vector widths and

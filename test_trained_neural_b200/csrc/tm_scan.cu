@@ -295,7 +295,7 @@ Plan plan_of(int B, int H, int T, int d) {
   const long long warps = (long long)B * H * ((d + CW - 1) / CW);
   const long long want = (long long)kSMs * (getenv("TMW") ? atoi(getenv("TMW")) : 16);
   long long S = want / warps;
-  const long long most = T / 64;                   // at least 64 tokens a segment
+  const long long most = T / 32;                   // at least 32 tokens a segment
   if (S > most) S = most;
   if (S < 3) S = 1;
   p.L = (int)(((T + S - 1) / S + kTile - 1) / kTile * kTile);

@@ -48,7 +48,7 @@ Plan plan_of(int B, int H, int G, int T, int d, int N) {
   // gradient sums and the joins, so it has to at least double the CTAs
   const long long ctas = (long long)B * H * p.blocks * p.warps / MAXW + 1;
   long long S = 3LL * kSMs / ctas;
-  const long long most = T / 64;
+  const long long most = T / TF;
   if (S > most) S = most;
   if (S < 2) S = 1;
   p.L = (int)(((T + S - 1) / S + TF - 1) / TF * TF);
