@@ -437,8 +437,9 @@ TM_API tm_status tm_scan(int B, int H, int G, int T, int d, int N, tm_dtype dtyp
 
 /*
  * Gradients of sum <dy, y> + <dstate_end, state_end> for the tm_scan call with
- * these inputs; the forward is recomputed inside (the states at every 8th token
- * are kept in the workspace).
+ * these inputs; the forward is recomputed inside: the states at every 4th token
+ * are kept in the workspace, as many bytes for each channel of each token as N
+ * rounded up to 8, 16, 32, 64 or 128.
  *   dy [B, H, T, d] dtype; dstate_end [B, H, d, N] or NULL (= zeros)
  *   dx, ddt, dz [B, H, T, d] dtype, strided (dz if and only if z);
  *   dB, dC [B, G, T, N] dtype, contiguous, summed over the heads of a group;

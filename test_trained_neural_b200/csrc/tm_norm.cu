@@ -7,9 +7,16 @@
 // One token: a row's channels sit in the registers of LPR lanes, so x is read
 // once, and mean and variance are two passes over registers. A sequence: one
 // pass for the statistics (per-thread sums about the thread's first value,
-// joined as (count, mean, sum of squared differences)), one for the output.
-// Bound by HBM. The parameters' gradients leave each CTA as one partial and
-// are summed in a fixed order.
+// joined as (count, mean, sum of squared differences)), one for the output,
+// which finds most of x in L2. HBM bounds it, and close behind it the issue
+// slots: two channels per instruction. The parameters' gradients leave each CTA
+// as one partial and are summed in a fixed order. Grids are one wave of CTAs
+// that walk their rows with the next ones in flight. Measured on B200:
+//   token by token, 4 x 8 x 8192 x 64 bf16, SiLU: 15.6 us, 4.4 TB/s (a CTA per
+//     128 rows: 18.2 us);
+//   its gradient, 8 x 8 x 8192 x 128 bf16: 84 us + 2.5 us for the sums, 4.8 TB/s
+//     (256-thread CTAs in 4.1 waves: 96 us; one channel per instruction: 109 us);
+//   a sequence, 2 x 4001 x 1536 fp32, 32 groups: 10.8 + 4.8 + 13.7 us.
 #include "tm_mixer.cuh"
 
 namespace tmem {

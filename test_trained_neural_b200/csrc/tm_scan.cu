@@ -34,9 +34,11 @@ struct Smem {
 // One segment of the sequence for one block of channels; LOCAL: only the state
 // that the segment leaves from a zero (segment 0: the initial) state.
 //
-// Bound by the special-function unit: one exp per (token, channel, state) at 16
-// a clock and SM. The rest of the recurrence is written for pairs of channels
-// (fma.rn.f32x2), which halves its issue slots.
+// Measured on B200, one prompt of 8192 x 2048 bf16 with 16 states in 37
+// segments: 81 us (LOCAL) + 7 us (joining) + 110 us, the special-function unit
+// busy for 0.77 and 0.65 of the two. One channel per instruction and tiles
+// through registers measured 130 and 209 us; 8, 12 and 20 warps an SM instead of
+// 16 (other segment counts) 275, 237 and 274 us where 16 took 227.
 template <typename T, int NL, int CPL, int V, int W, bool LOCAL>
 __global__ void __launch_bounds__(32 * W, (NL >= 16 ? 8 : 16) / W) scan_kernel(const Scan a, const Plan pl, float *hloc, float *esum) {
   using S = Smem<T, NL, CPL, V, W>;
@@ -142,10 +144,15 @@ __global__ void __launch_bounds__(32 * W, (NL >= 16 ? 8 : 16) / W) scan_kernel(c
 #pragma unroll
       for (int s = 0; s < SPL; ++s) {
         const bool live = in && n0 + s < N;
-        Af[c][s] = live ? a.A[(ch0 + c0 + c) * N + n0 + s] * kLog2e : 0.f;
-        hf[c][s] = live && a.state0 && seg == 0 ? a.state0[(chan + c) * N + n0 + s] : 0.f;
+        Af[c][s] = live ? rate(a.A[(ch0 + c0 + c) * N + n0 + s]) : 0.f;
+        hf[c][s] = live && a.state0 && seg == 0 && (LOCAL || pl.S == 1) ? a.state0[(chan + c) * N + n0 + s] : 0.f;
       }
-      if (!LOCAL && seg > 0 && in) lds<SPL>(hf[c], hloc + ((seg - 1) * per + chan + c) * NP + n0);
+      // The state before segment 0 of a split sequence comes from the copy that
+      // the LOCAL launch leaves behind the segments' ends: state_end may be
+      // state0, and the last segment may be done before segment 0 begins.
+      float *from = hloc + ((seg > 0 ? seg - 1 : pl.S - 1) * per + chan + c) * NP + n0;
+      if (LOCAL && seg == 0 && in) sts<SPL>(from, hf[c]);
+      if (!LOCAL && pl.S > 1 && in) lds<SPL>(hf[c], from);
     }
 #pragma unroll
     for (int c = 0; c < C2; ++c)
@@ -316,7 +323,7 @@ cudaError_t run(const Scan &c, const Plan &p, cudaStream_t st) {
       if (e != cudaSuccess) return e;
     }
   float *hloc = static_cast<float *>(c.ws);
-  float *esum = hloc + (size_t)(p.S - 1) * c.B * c.H * c.d * NL * SPL;
+  float *esum = hloc + (size_t)p.S * c.B * c.H * c.d * NL * SPL;
   if (p.S > 1) {
     local<<<(unsigned)(units * (p.S - 1)), 32 * W, smem, st>>>(c, p, hloc, esum);
     cudaError_t e = cudaGetLastError();
@@ -389,7 +396,7 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const Scan a, const long
 #pragma unroll
   for (int s = 0; s < SPL; ++s) {
     const bool live = n0 + s < N;
-    hs[s] = fmaf(ex2(e * (A[s] * kLog2e)), hs[s], e * x * (live ? to_f(Bp[s]) : 0.f));
+    hs[s] = fmaf(ex2(e * rate(A[s])), hs[s], e * x * (live ? to_f(Bp[s]) : 0.f));
     y = fmaf(live ? to_f(Cp[s]) : 0.f, hs[s], y);
   }
 #pragma unroll
@@ -433,7 +440,7 @@ size_t ws_of(int B, int H, int G, int T, int d) {
   size_t most = 0;
   for (const bool joined : {false, true}) {
     const Plan p = joined ? plan_of<NL, 4>(B, G, T, H / G * d) : plan_of<NL, 4>(B, H, T, d);
-    if ((size_t)(p.S - 1) > most) most = p.S - 1;
+    if (p.S > 1 && (size_t)p.S > most) most = p.S;
   }
   return up256(most * B * H * d * (NL * SPL + 1) * 4);
 }

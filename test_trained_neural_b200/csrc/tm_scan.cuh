@@ -8,9 +8,12 @@
 // Layout of the work: NL lanes share a channel, each with 4 consecutive
 // states (N <= 4 NL, the rest padded with A = B = C = 0, which leaves them
 // zero), and a lane owns CPL channels, so a warp covers 32 / NL * CPL channels
-// and a lane's B_t and C_t are one 16-byte shared-memory load each for
-// 4 CPL state updates. Sums over the states of a channel end with a few
-// shuffles in which the lanes exchange halves of their channels.
+// and what it loads of B_t and C_t serves 4 CPL state updates. The arithmetic is
+// for pairs of channels (fma.rn.f32x2).
+//
+// What bounds it: one exp per (token, channel, state) on the special-function
+// unit, 16 a clock and SM (2.7e8 of them, 8192 x 2048 x 16, take 60 us at 1.9
+// GHz; HBM needs 21 us for the tokens), and close behind it the issue slots.
 #pragma once
 #include "tm_mixer.cuh"
 
@@ -19,12 +22,12 @@ namespace mix {
 
 constexpr int SPL = 4;               // states a lane holds of each of its channels
 
-// Sum of M values per lane over NL lanes that are STEP apart: at each step a
-// lane passes on half of its values and adds what it gets to the other half,
-// so a value costs about one shuffle. Afterwards lane number nl of them holds
-// the totals of the values first(nl) .. first(nl) + kept - 1 in v[0 ..]
-// (when NL > M, lanes that agree in their low log2(M) bits hold the same one).
-template <int M, int NL, int STEP = 1>
+// Sum of M values per lane over the NL lanes of a channel: at each step a lane
+// passes on half of its values and adds what it gets to the other half, so a
+// value costs about one shuffle. Afterwards lane nl holds the totals of the
+// values first(nl) .. first(nl) + kept - 1 in v[0 ..] (when NL > M, lanes that
+// agree in their low log2(M) bits hold the same one).
+template <int M, int NL>
 struct LaneSum {
   static constexpr int kept = M >= NL ? M / NL : 1;
   static constexpr int writers = M < NL ? M : NL;      // lanes below this number hold every total once
@@ -38,11 +41,11 @@ struct LaneSum {
         for (int i = 0; i < M / 2; ++i)
           if (i < m / 2) {
             const float keep = up ? v[i + m / 2] : v[i], send = up ? v[i] : v[i + m / 2];
-            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, bit * STEP);
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, bit);
           }
         m /= 2;
       } else {
-        v[0] += __shfl_xor_sync(0xffffffffu, v[0], bit * STEP);
+        v[0] += __shfl_xor_sync(0xffffffffu, v[0], bit);
       }
     }
   }
@@ -58,6 +61,13 @@ struct LaneSum {
     return f;
   }
 };
+
+// A in base-2 exponents, held to finite values: e = 0 (a row behind the end, a
+// token that writes nothing) has to leave a decay of 1 whatever A is.
+__device__ __forceinline__ float rate(float A) {
+  const float r = A * kLog2e;
+  return isinf(r) ? copysignf(3.e38f, r) : r;
+}
 
 // Lanes that share a channel for N states.
 inline int lanes_of(int N) {
@@ -92,7 +102,7 @@ static __global__ void __launch_bounds__(128) join_segments_kernel(const Scan a,
   const long long chan = i / NP;
   const int n = (int)(i - chan * NP);
   if (chan >= per) return;
-  const float A2 = n < a.N ? a.A[(chan % ((long long)a.H * a.d)) * a.N + n] * kLog2e : 0.f;
+  const float A2 = n < a.N ? rate(a.A[(chan % ((long long)a.H * a.d)) * a.N + n]) : 0.f;
   const bool back = blockIdx.y == 1;
   float *p = (back ? start : end) + i;
   float v = back ? (n < a.N && a.dstate_end ? a.dstate_end[chan * a.N + n] : 0.f) : *p;

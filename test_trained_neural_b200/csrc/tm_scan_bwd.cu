@@ -16,6 +16,12 @@
 // and also forms what the segment adds to the gradient that enters it from
 // behind, sum_t (prod a up to t) Cm_t k_t; the second joins the segments before
 // (state) and after (gradient) its own, with the segments' decays exp(A sum e).
+//
+// Measured on B200, 4 x 8 x 8192 x 64 bf16, 16 states, 13 segments: first pass
+// 142 us, second 376 us, at 11 warps an SM half of the issue slots used, the
+// special-function unit 0.38: the dependent chains of a chunk bound it. Holding
+// the decays of a chunk instead of evaluating them again spills (513 us); chunks
+// of 8 at 8 warps an SM took 609 us; the states in shared memory at 16 warps 407.
 #include "tm_scan.cuh"
 
 namespace tmem {
@@ -181,7 +187,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) states_kernel(const Scan a, co
 #pragma unroll
     for (int c = 0; c < CPL; ++c) {
       const bool live = c_blk + c0 + c < a.d && n0 + s < N;
-      A[c] = live ? a.A[(hd + c0 + c) * N + n0 + s] * kLog2e : 0.f;
+      A[c] = live ? rate(a.A[(hd + c0 + c) * N + n0 + s]) : 0.f;
       h[c] = live && a.state0 && w.seg == 0 ? a.state0[(chan + c) * N + n0 + s] : 0.f;
     }
     A2[s] = pair(A[0], A[1]);
@@ -446,7 +452,7 @@ __global__ void __launch_bounds__(32 * W, 12 / W) grad_kernel(const Scan a, cons
 #pragma unroll
       for (int s = 0; s < SPL; ++s) {
         const bool live = c_blk + c0 + c < a.d && n0 + s < N;
-        Af[c][s] = live ? a.A[(hd + c0 + c) * N + n0 + s] * kLog2e : 0.f;
+        Af[c][s] = live ? rate(a.A[(hd + c0 + c) * N + n0 + s]) : 0.f;
         Rf[c][s] = live && a.dstate_end ? a.dstate_end[(chan + c) * N + n0 + s] : 0.f;
         hf[c][s] = 0.f;
       }

@@ -317,6 +317,80 @@ def test_scan_steps_continue_a_prompt(B, H, G, d, N, kind, sliced):
     close(state, f64(last), 2 * scan_tol(T + more, N))
 
 
+@pytest.mark.parametrize("T", [20, 400])
+def test_scan_decay_of_the_lowest_values(T):
+    """A of -inf and of fp32's lowest value: every token alone where it writes, and the state left alone by rows
+    behind the end and by tokens whose e is 0 (softplus(-200))."""
+    r, c, o = scan_case(2, 1, 1, T, 16, 16, F, lengths=[T, 7])
+    c["A"][:, :8] = float("-inf")
+    c["A"][:, 8:] = torch.finfo(F).min
+    c["dt"][0, :, 11:] = -200.0
+    n = lens([T, 7])
+    y, end = tm.selective_scan(**c, **o, lengths=n)
+    assert torch.isfinite(end).all() and torch.isfinite(y[0]).all()
+    # sequence 0: the state stays what token 10 wrote; sequence 1: what token 6 wrote
+    for b, t in ((0, 10), (1, 6)):
+        e = np.logaddexp(f64(c["dt"][b, 0, t]) + f64(o["dt_bias"][0]), 0.0)
+        want = (e * f64(c["x"][b, 0, t]))[:, None] * f64(c["Bm"][b, 0, t])
+        close(end[b, 0], want, 64 * U)
+    dy = poison(r.tokens(2, 1, T, 16, F), [T, 7])
+    g = tm.selective_scan_backward(**c, dy=dy, **o, lengths=n)
+    for k in ("dx", "dB", "dC", "dz", "dstate"):
+        assert torch.isfinite(g[k]).all(), k
+
+
+def test_expanded_inputs():
+    """x itself repeated over the batch: outputs are whole tensors of their own."""
+    r = Draw("expand")
+    B, H, T, d, N = 3, 2, 40, 16, 16
+    x = r.normal(1, H, T, d, kind=BF).expand(B, H, T, d)
+    f, w = r.normal(H, d, 4), r.normal(H, d)
+    _, c, o = scan_case(B, H, 1, T, d, N, BF)
+    c["x"] = x
+    whole = {**c, "x": x.contiguous()}
+    dy = r.normal(B, H, T, d, kind=BF)
+    st = tm.group_norm(x, w)[1]
+    for got, want in ((tm.short_conv(x, f), tm.short_conv(x.contiguous(), f)),
+                      (tm.short_conv_backward(x, f, dy), tm.short_conv_backward(x.contiguous(), f, dy)),
+                      (tm.selective_scan(**c, **o), tm.selective_scan(**whole, **o)),
+                      (tm.selective_scan_backward(**c, dy=dy, **o), tm.selective_scan_backward(**whole, dy=dy, **o)),
+                      (tm.group_norm(x, w), tm.group_norm(x.contiguous(), w)),
+                      (tm.group_norm_backward(x, dy, st, w), tm.group_norm_backward(x.contiguous(), dy, st, w))):
+        for p, q in zip(flat(got), flat(want)):
+            assert torch.equal(p, q)
+
+
+def test_offsets_past_32_bits():
+    """2^31 elements and more in one tensor: the last rows are those of a call on the end alone."""
+    d, T = 2048, (1 << 20) + 77
+    r = Draw("long")
+    x = torch.empty(1, 1, T, d, device="cuda", dtype=BF)
+    for i in range(0, T, 1 << 16):
+        x[0, 0, i:i + (1 << 16)] = r.normal(min(1 << 16, T - i), d, kind=BF)
+    f, w = r.normal(1, d, 4), r.normal(1, d)
+    n = 300
+    y, tail = tm.short_conv(x, f)
+    end, tail_end = tm.short_conv(x[:, :, -n:], f, hist=x[:, :, -n - 3:-n].contiguous())
+    assert torch.equal(y[:, :, -n:], end) and torch.equal(tail, tail_end)
+    g = tm.short_conv_backward(x, f, y)["dx"]
+    g_end = tm.short_conv_backward(x[:, :, -n:], f, y[:, :, -n:], hist=x[:, :, -n - 3:-n].contiguous())["dx"]
+    assert torch.equal(g[:, :, -n:], g_end)
+    del g, y
+    y, st = tm.group_norm(x, w)
+    assert torch.equal(y[:, :, -n:], tm.group_norm(x[:, :, -n:], w)[0])
+    del y
+    # the scan forgets within a few hundred tokens (e A below -0.3): its end does not know its beginning
+    A = torch.full((1, d, 16), -4.0, device="cuda")
+    bias = torch.full((1, d), -2.0, device="cuda")
+    Bm = r.normal(1, 1, T, 16, kind=BF)
+    y, state = tm.selective_scan(x, torch.zeros_like(x), A, Bm, Bm, dt_bias=bias)
+    y_end, state_end = tm.selective_scan(x[:, :, -n:], torch.zeros_like(x[:, :, -n:]), A, Bm[:, :, -n:], Bm[:, :, -n:],
+                                         dt_bias=bias)
+    # e = softplus(-2) = 0.127: exp(-0.5 n / 2) of the difference is left after half of the rows
+    close(state, f64(state_end), scan_tol(n, 16))
+    close(y[:, :, -n // 2:], f64(y_end[:, :, -n // 2:]), 2 * half(BF))
+
+
 def test_scan_state_in_place_and_broadcast_inputs():
     """state_end = state, a B and C shared by the batch (stride 0) and a z that repeats over heads."""
     B, H, T, d, N = 3, 2, 200, 16, 16
@@ -352,6 +426,10 @@ NORM = [  # B, H, T, d, kind, out, layout, over, act, affine, lengths
     (1, 2, 5, 1024, F, F, "bthd", "token", "silu", True, None),
     (1, 1, 7, 3001, F, F, "bhtd", "token", "silu", True, [5]),          # a row beyond the registers
     (2, 1, 4, 1536, BF, BF, "odd", "token", None, True, None),
+    (2, 1, 9, 2048, BF, BF, "bhtd", "token", "silu", True, [9, 4]),     # a row over a whole block
+    (1, 1, 5, 4096, BF, F, "bthd", "token", "silu", True, None),
+    (1, 1, 3, 8200, BF, BF, "bhtd", "token", None, True, None),
+    (1, 2, 6, 4100, F, F, "bhtd", "token", "silu", True, None),
     (2, 4, 50, 8, BF, BF, "bthd", "sequence", "silu", True, None),
     (3, 2, 300, 24, F, F, "bhtd", "sequence", "silu", True, [300, 0, 1]),
     (2, 32, 130, 48, F, F, "bthd", "sequence", "silu", True, [130, 77]),
@@ -477,6 +555,19 @@ def test_other_stream():
         side.synchronize()
         del junk
         assert all(torch.equal(p, q) for p, q in zip(got, want[name])), name
+
+
+def test_two_streams_at_once():
+    """The same calls on two streams at the same time, each with its own buffers."""
+    calls = all_calls(Draw("two"))
+    want = {k: flat(v()) for k, v in calls.items()}
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = [[(k, flat(v(stream=s))) for k, v in calls.items() if k != "steps"] for _ in range(3) for s in (one, two)]
+    torch.cuda.synchronize()
+    for each_call in got:
+        for k, out in each_call:
+            assert all(torch.equal(p, q) for p, q in zip(out, want[k])), k
 
 
 def test_captured_and_replayed():
