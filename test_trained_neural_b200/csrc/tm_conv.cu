@@ -7,11 +7,11 @@
 // All of it is one pass over the tokens: HBM bounds it, and close behind it the
 // issue slots, so the arithmetic is written for two channels per instruction
 // (fma.rn.f32x2: at one channel per instruction the gradient took 62 us where it
-// now takes 31). A thread owns V consecutive channels and walks a run of rows;
+// now takes 29). A thread owns V consecutive channels and walks a run of rows;
 // the w - 1 rows before a run come from L2. Measured on B200, bf16, w = 4:
 //   forward, 65536 x 2048 (16 heads of 128 in [T, H, d] rows): 93 us, 5.8 TB/s
 //     (with rows by plain loads one batch ahead: 109 us; short runs: 111 us);
-//   gradient, 4 x 8 x 8192 x 64: 31 us + 3 us for the sums, 2.9 TB/s, bound by
+//   gradient, 4 x 8 x 8192 x 64: 29 us + 3 us for the sums, 3.1 TB/s, bound by
 //     latency at 12 warps an SM (a run is 76 rows at this size; slots in shared
 //     memory as in the forward measured 34 us);
 //   one token, 64 x 1536: 3.1 us, a launch.
@@ -183,15 +183,14 @@ __global__ void __launch_bounds__(NT, 2) conv_kernel(const Conv a, const Split s
 template <typename T, int V, int MAXW, bool EXACT, int RB>
 __global__ void __launch_bounds__(BT, 3) conv_backward_kernel(const Conv a, const Split sp, float *part) {
   const int run = sp.run;
-  extern __shared__ __align__(16) float red[];               // [threads][V]
+  extern __shared__ __align__(16) float red[];               // [w + 1][threads][V]
   unsigned blk = blockIdx.x;
   const int tile = blk % sp.tiles;
   blk /= sp.tiles;
   const int cb = blk % sp.cb;
   blk /= sp.cb;
   const int h = blk % a.H, b = blk / a.H;
-  const int vi = threadIdx.x % sp.nvb, rl = threadIdx.x / sp.nvb;
-  const int v = cb * sp.nvb + vi;
+  const int rl = threadIdx.x / sp.nvb, v = cb * sp.nvb + threadIdx.x % sp.nvb;
   const bool mine = v < sp.nv;
   const int c = v * V, w = a.w, d = a.d;
   const int n = tokens_of(a.lengths, b, a.T);
@@ -320,20 +319,17 @@ __global__ void __launch_bounds__(BT, 3) conv_backward_kernel(const Conv a, cons
   }
   // partial sums of the CTA: [b, tile][h, c, w + 1]
   float *out = part + (((long long)b * sp.tiles + tile) * a.H + h) * d * (w + 1);
+  const int pitch = blockDim.x * V, cols = sp.nvb * V;
 #pragma unroll
-  for (int j = 0; j <= MAXW; ++j) {
-    if (j < MAXW && j >= w) continue;
-    sts<V>(red + threadIdx.x * V, j < MAXW ? df[j < MAXW ? j : 0] : db);
-    __syncthreads();
-    if (rl == 0 && mine) {
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        float s = 0.f;
-        for (int r = 0; r < sp.RL; ++r) s += red[(r * sp.nvb + vi) * V + e];
-        out[(long long)(c + e) * (w + 1) + (j < MAXW ? j : w)] = s;
-      }
-    }
-    __syncthreads();
+  for (int j = 0; j <= MAXW; ++j)
+    if (j == MAXW || j < w) sts<V>(red + (j < MAXW ? j : w) * pitch + threadIdx.x * V, j < MAXW ? df[j < MAXW ? j : 0] : db);
+  __syncthreads();
+  for (int i = threadIdx.x; i < cols * (w + 1); i += blockDim.x) {
+    const int j = i / cols, k = i - j * cols, ch = cb * cols + k;
+    if (ch >= d) continue;
+    float s = 0.f;
+    for (int r = 0; r < sp.RL; ++r) s += red[j * pitch + r * cols + k];
+    out[(long long)ch * (w + 1) + j] = s;
   }
 }
 
@@ -471,7 +467,7 @@ cudaError_t conv_backward_launch(Conv c, cudaStream_t st) {
     const long long grid = (long long)sp.tiles * sp.cb * c.B * c.H;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
     const int threads = sp.nvb * sp.RL;
-    kern<<<(unsigned)grid, threads, threads * V * sizeof(float), st>>>(c, sp, part);
+    kern<<<(unsigned)grid, threads, (c.w + 1) * threads * V * sizeof(float), st>>>(c, sp, part);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const long long ch = (long long)c.H * c.d, n = ch * (c.w + 1);
