@@ -192,6 +192,7 @@ __global__ void __launch_bounds__(BT, 3) conv_backward_kernel(const Conv a, cons
   const int h = blk % a.H, b = blk / a.H;
   const int rl = threadIdx.x / sp.nvb, v = cb * sp.nvb + threadIdx.x % sp.nvb;
   const bool mine = v < sp.nv;
+  let_next_start();
   const int c = v * V, w = a.w, d = a.d;
   const int n = tokens_of(a.lengths, b, a.T);
   const long long bh = (long long)b * a.H + h;
@@ -338,6 +339,7 @@ __global__ void __launch_bounds__(BT, 3) conv_backward_kernel(const Conv a, cons
 __global__ void __launch_bounds__(256) conv_sum_kernel(const float *part, int parts, long long ch, int w, float *dfilt,
                                                        float *dbias) {
   __shared__ float red[8][32];
+  after_previous();
   const long long n = ch * (w + 1);
   const long long i = (long long)blockIdx.x * 32 + threadIdx.x % 32;
   const int k = threadIdx.x / 32;
@@ -471,8 +473,8 @@ cudaError_t conv_backward_launch(Conv c, cudaStream_t st) {
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const long long ch = (long long)c.H * c.d, n = ch * (c.w + 1);
-    conv_sum_kernel<<<(unsigned)((n + 31) / 32), 256, 0, st>>>(part, c.B * sp.tiles, ch, c.w, c.dfilt, c.dbias);
-    return cudaGetLastError();
+    return launch_next(conv_sum_kernel, dim3((unsigned)((n + 31) / 32)), 256, 0, st, part, c.B * sp.tiles, ch, c.w, c.dfilt,
+                       c.dbias);
   };
   auto pick = [&](auto t) {
     using T = decltype(t);

@@ -302,6 +302,13 @@ __device__ __forceinline__ F2 ex2_again(F2 x) {
   return pair(a, b);
 }
 
+// A call's later launches begin while the earlier one drains: every kernel that
+// another of the call follows lets it be launched once all of its own blocks
+// run, and the follower waits here, for everything before it to be complete and
+// visible, before it touches what that wrote. (A no-op in a call's first launch.)
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Tokens of sequence b: the caller's length held to [0, T].
 __device__ __forceinline__ int tokens_of(const int *lengths, int b, int T) {
   return lengths ? min(max(lengths[b], 0), T) : T;

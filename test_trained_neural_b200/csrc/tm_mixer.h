@@ -66,6 +66,23 @@ cudaError_t norm_backward_launch(Norm c, cudaStream_t st);
 size_t norm_ws(int B, int H, int T, int d, Over over);
 size_t norm_backward_ws(int B, int H, int T, int d, Over over);
 
+// Launch of a kernel that follows another one of the same call and waits for it
+// by itself (after_previous()): saves the 1 to 2 us between dependent launches.
+template <typename... P, typename... A>
+cudaError_t launch_next(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
+
 // Whether vectors of V elements of `el` bytes fit a tensor: its base address,
 // its strides and the row length are whole vectors.
 inline bool fits(const void *p, const Str &s, int d, int V, int el) {

@@ -187,6 +187,7 @@ __global__ void __launch_bounds__(LPR > GT ? LPR : GT) token_backward_kernel(con
   extern __shared__ __align__(16) float red[];          // [threads][V]
   constexpr int CTA = LPR > GT ? LPR : GT;
   __shared__ float sums[2][CTA / 32];
+  let_next_start();
   constexpr int ROWS = CTA / LPR, P = (V + 1) / 2;
   const int tile = blockIdx.x % tiles, bh = blockIdx.x / tiles;
   const int h = bh % a.H, b = bh / a.H, d = a.d;
@@ -301,6 +302,7 @@ __global__ void __launch_bounds__(LPR > GT ? LPR : GT) token_backward_kernel(con
 template <typename TI, typename TO>
 __global__ void __launch_bounds__(NT) token_wide_backward_kernel(const Norm a, const int tiles, float *part) {
   __shared__ float red[NT / 32];
+  let_next_start();
   const int tile = blockIdx.x % tiles, bh = blockIdx.x / tiles;
   const int h = bh % a.H, b = bh / a.H, d = a.d;
   const int n = tokens_of(a.lengths, b, a.T);
@@ -389,6 +391,7 @@ __device__ __forceinline__ At at_of(const Norm &a, const Cols &s, int V) {
 template <typename TI, int V>
 __global__ void __launch_bounds__(NT) seq_stats_kernel(const Norm a, const Cols s, float2 *part) {
   __shared__ float3 red[NT];
+  let_next_start();
   const At q = at_of(a, s, V);
   const int n = tokens_of(a.lengths, q.b, a.T);
   float3 mine = make_float3(0.f, 0.f, 0.f);
@@ -442,6 +445,8 @@ __global__ void __launch_bounds__(NT) seq_stats_kernel(const Norm a, const Cols 
 __global__ void __launch_bounds__(NT) seq_join_kernel(const Norm a, const Cols s, const int V, const float2 *part,
                                                       float2 *stats) {
   __shared__ double red[2][NT / 32];
+  let_next_start();
+  after_previous();
   const int bh = blockIdx.x, h = bh % a.H, b = bh / a.H;
   const int n = tokens_of(a.lengths, b, a.T);
   const int vh = a.d / V, vecs = a.H * vh;
@@ -481,6 +486,7 @@ __global__ void __launch_bounds__(NT) seq_join_kernel(const Norm a, const Cols s
 
 template <typename TI, typename TO, int V>
 __global__ void __launch_bounds__(NT) seq_apply_kernel(const Norm a, const Cols s, const float2 *stats) {
+  after_previous();
   const At q = at_of(a, s, V);
   if (!q.mine) return;
   const int n = tokens_of(a.lengths, q.b, a.T);
@@ -515,6 +521,7 @@ __global__ void __launch_bounds__(NT) seq_apply_kernel(const Norm a, const Cols 
 template <typename TI, typename TO, int V>
 __global__ void __launch_bounds__(NT) seq_sums_kernel(const Norm a, const Cols s, float *part) {
   __shared__ __align__(16) float red[NT * V];
+  let_next_start();
   const At q = at_of(a, s, V);
   const int n = tokens_of(a.lengths, q.b, a.T);
   Pairs<V> dw, db;
@@ -576,6 +583,8 @@ __global__ void __launch_bounds__(NT) seq_join_sums_kernel(const Norm a, const i
                                                            float2 *means) {
   __shared__ float slice[2][8][32];
   __shared__ float tot[2][32];
+  let_next_start();
+  after_previous();
   const int bh = blockIdx.x, h = bh % a.H, b = bh / a.H, d = a.d;
   const long long hd = (long long)a.H * d;
   const int l = threadIdx.x % 32, k = threadIdx.x / 32;
@@ -625,6 +634,8 @@ __global__ void __launch_bounds__(NT) seq_join_sums_kernel(const Norm a, const i
 
 template <typename TI, typename TO, int V>
 __global__ void __launch_bounds__(NT) seq_grad_kernel(const Norm a, const Cols s, const float2 *means) {
+  let_next_start();
+  after_previous();
   const At q = at_of(a, s, V);
   if (!q.mine) return;
   const int n = tokens_of(a.lengths, q.b, a.T);
@@ -669,6 +680,7 @@ __global__ void __launch_bounds__(NT) seq_grad_kernel(const Norm a, const Cols s
 __global__ void __launch_bounds__(256) pair_sum_kernel(const float *part, int parts, long long hd, float *dweight,
                                                        float *dbias) {
   __shared__ float red[8][32];
+  after_previous();
   const long long n = 2 * hd, i = (long long)blockIdx.x * 32 + threadIdx.x % 32;
   const int k = threadIdx.x / 32;
   float s = 0.f;
@@ -688,8 +700,7 @@ __global__ void __launch_bounds__(256) pair_sum_kernel(const float *part, int pa
 }
 cudaError_t pair_sum(const float *part, int parts, long long hd, float *dweight, float *dbias, cudaStream_t st) {
   if (!dweight && !dbias) return cudaSuccess;
-  pair_sum_kernel<<<(unsigned)((2 * hd + 31) / 32), 256, 0, st>>>(part, parts, hd, dweight, dbias);
-  return cudaGetLastError();
+  return launch_next(pair_sum_kernel, dim3((unsigned)((2 * hd + 31) / 32)), 256, 0, st, part, parts, hd, dweight, dbias);
 }
 
 // CTAs of a (batch, head) that share its rows token by token: together one wave
@@ -747,11 +758,9 @@ cudaError_t forward(const Norm &a, cudaStream_t st) {
     stats<<<(unsigned)grid, threads, 0, st>>>(a, s, part);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    seq_join_kernel<<<(unsigned)bh, NT, 0, st>>>(a, s, VV, part, st2);
-    e = cudaGetLastError();
+    e = launch_next(seq_join_kernel, dim3((unsigned)bh), NT, 0, st, a, s, VV, part, st2);
     if (e != cudaSuccess) return e;
-    apply<<<(unsigned)grid, threads, 0, st>>>(a, s, st2);
-    return cudaGetLastError();
+    return launch_next(apply, dim3((unsigned)grid), threads, 0, st, a, s, st2);
   };
   if (vec) return go(seq_stats_kernel<TI, V>, seq_apply_kernel<TI, TO, V>, V);
   return go(seq_stats_kernel<TI, 1>, seq_apply_kernel<TI, TO, 1>, 1);
@@ -798,11 +807,9 @@ cudaError_t backward(const Norm &a, cudaStream_t st) {
     sums<<<(unsigned)grid, NT, 0, st>>>(a, s, part);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    seq_join_sums_kernel<<<(unsigned)bh, NT, 0, st>>>(a, s.tiles, part, chan, means);
-    e = cudaGetLastError();
+    e = launch_next(seq_join_sums_kernel, dim3((unsigned)bh), NT, 0, st, a, s.tiles, part, chan, means);
     if (e != cudaSuccess) return e;
-    grad<<<(unsigned)grid, NT, 0, st>>>(a, s, means);
-    e = cudaGetLastError();
+    e = launch_next(grad, dim3((unsigned)grid), NT, 0, st, a, s, means);
     return e != cudaSuccess ? e : pair_sum(chan, a.B, hd, a.dweight, a.dbias, st);
   };
   if (vec) return go(seq_sums_kernel<TI, TO, V>, seq_grad_kernel<TI, TO, V>, V);

@@ -123,7 +123,8 @@ __global__ void __launch_bounds__(32 * W, (NL >= 16 ? 8 : 16) / W) scan_kernel(c
     Bf += TQ * a.sB.t;
     Cf += TQ * a.sC.t;
   };
-  fetch(t_seg, 0);
+  if (LOCAL) let_next_start();
+  fetch(t_seg, 0);                                // the inputs are there, whatever launch of the call this is
 
   for (int i = tid; i < CB; i += nthr) {
     const bool in = c_blk + i < a.d;
@@ -138,6 +139,7 @@ __global__ void __launch_bounds__(32 * W, (NL >= 16 ? 8 : 16) / W) scan_kernel(c
   const long long chan = bh * a.d + c_blk + c0;         // the lane's first channel among them
   {
     float Af[CPL][SPL], hf[CPL][SPL];
+    if (!LOCAL) after_previous();
 #pragma unroll
     for (int c = 0; c < CPL; ++c) {
       const bool in = c_blk + c0 + c < a.d;
@@ -330,7 +332,8 @@ cudaError_t run(const Scan &c, const Plan &p, cudaStream_t st) {
     if (e == cudaSuccess && p.S > 2) e = join_segments(c, p.S, p.S - 2, NL * SPL, hloc, nullptr, esum, st);
     if (e != cudaSuccess) return e;
   }
-  whole<<<(unsigned)(units * p.S), 32 * W, smem, st>>>(c, p, hloc, esum);
+  if (p.S > 1) return launch_next(whole, dim3((unsigned)(units * p.S)), 32 * W, smem, st, c, p, hloc, esum);
+  whole<<<(unsigned)units, 32 * W, smem, st>>>(c, p, hloc, esum);
   return cudaGetLastError();
 }
 

@@ -98,6 +98,8 @@ inline void collapse(Scan &c, std::initializer_list<Str *> ss) {
 static __global__ void __launch_bounds__(128) join_segments_kernel(const Scan a, const int S, const int last, const int NP,
                                                                    float *end, float *start, const float *esum) {
   constexpr int U = 8;
+  let_next_start();
+  after_previous();
   const long long per = (long long)a.B * a.H * a.d, i = (long long)blockIdx.x * 128 + threadIdx.x;
   const long long chan = i / NP;
   const int n = (int)(i - chan * NP);
@@ -129,8 +131,7 @@ inline cudaError_t join_segments(const Scan &a, int S, int last, int NP, float *
                                  cudaStream_t st) {
   const long long n = (long long)a.B * a.H * a.d * NP, grid = (n + 127) / 128;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-  join_segments_kernel<<<dim3((unsigned)grid, start ? 2 : 1), 128, 0, st>>>(a, S, last, NP, end, start, esum);
-  return cudaGetLastError();
+  return launch_next(join_segments_kernel, dim3((unsigned)grid, start ? 2 : 1), 128, 0, st, a, S, last, NP, end, start, esum);
 }
 
 }  // namespace mix

@@ -177,6 +177,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) states_kernel(const Scan a, co
     Bf += TF * a.sB.t;
     Cf += TF * a.sC.t;
   };
+  let_next_start();
   fetch(t_seg, 0);
   for (int i = tid; i < CB; i += nthr) s_bias[i] = c_blk + i < a.d && a.dt_bias ? a.dt_bias[hd + i] : 0.f;
 
@@ -332,6 +333,9 @@ __global__ void __launch_bounds__(32 * W, 12 / W) grad_kernel(const Scan a, cons
   const long long hd = (long long)w.h * a.d + c_blk;
   const float *ck = ws + pl.ck, *cume = ws + pl.cume;
   const bool idle = c_blk + warp * CW >= a.d;           // a warp beyond the head's channels only stages
+
+  let_next_start();
+  after_previous();
 
   const T *xp = static_cast<const T *>(a.x) + w.b * a.sx.b + w.h * a.sx.h + c_blk;
   const T *dp = static_cast<const T *>(a.dt) + w.b * a.sdt.b + w.h * a.sdt.h + c_blk;
@@ -735,6 +739,8 @@ __global__ void __launch_bounds__(32 * W, 12 / W) grad_kernel(const Scan a, cons
 // dB and dC: the partials of the channel blocks that share them, in order.
 template <typename T>
 __global__ void __launch_bounds__(256) join_bc_kernel(const Scan a, const Plan pl, const float *bc) {
+  let_next_start();
+  after_previous();
   const long long rows = (long long)a.B * a.G * a.T, i = (long long)blockIdx.x * 256 + threadIdx.x;
   const int lg = __ffs(2 * pl.NP) - 1;                  // 2 NP is a power of two
   const long long row = i >> lg;
@@ -751,6 +757,7 @@ __global__ void __launch_bounds__(256) join_bc_kernel(const Scan a, const Plan p
 // dA, dD and d(dt_bias): the partials of the sequences and segments, in order.
 __global__ void __launch_bounds__(256) join_param_kernel(const Scan a, const Plan pl, const float *ws) {
   __shared__ float red[8][32];
+  after_previous();
   const long long HD = (long long)a.H * a.d, nA = HD * pl.NP, n = nA + 2 * HD;
   const long long i = (long long)blockIdx.x * 32 + threadIdx.x % 32;
   const int k = threadIdx.x / 32, parts = a.B * pl.S;
@@ -796,17 +803,14 @@ cudaError_t run(const Scan &c, const Plan &p, cudaStream_t st) {
     e = cudaFuncSetAttribute(grad, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm2);
     if (e != cudaSuccess) return e;
   }
-  grad<<<(unsigned)grid, thr, sm2, st>>>(c, p, ws);
-  e = cudaGetLastError();
+  e = launch_next(grad, dim3((unsigned)grid), thr, sm2, st, c, p, ws);
   if (e != cudaSuccess) return e;
   if (p.pbn > 1) {
-    join_bc_kernel<T><<<(unsigned)((nbc + 255) / 256), 256, 0, st>>>(c, p, ws + p.bc);
-    e = cudaGetLastError();
+    e = launch_next(join_bc_kernel<T>, dim3((unsigned)((nbc + 255) / 256)), 256, 0, st, c, p, ws + p.bc);
     if (e != cudaSuccess) return e;
   }
   const long long n = (long long)c.H * c.d * (NP + 2);
-  join_param_kernel<<<(unsigned)((n + 31) / 32), 256, 0, st>>>(c, p, ws);
-  return cudaGetLastError();
+  return launch_next(join_param_kernel, dim3((unsigned)((n + 31) / 32)), 256, 0, st, c, p, ws);
 }
 
 template <typename T, int NL, int VF, int VB>
