@@ -14,7 +14,7 @@
 //   gradient, 4 x 8 x 8192 x 64: 29 us + 3 us for the sums, 3.1 TB/s, bound by
 //     latency at 12 warps an SM (a run is 76 rows at this size; slots in shared
 //     memory as in the forward measured 34 us);
-//   one token, 64 x 1536: 3.1 us, a launch.
+//   one token, 64 x 1536: 2.3 us, a launch.
 #include <type_traits>
 
 #include "tm_mixer.cuh"
@@ -362,28 +362,31 @@ __global__ void __launch_bounds__(256) conv_sum_kernel(const float *part, int pa
 // moved on by a row. A thread owns V channels of one (batch, head); every row
 // of its channels is in registers before it writes, so the update is in place.
 template <typename T, int V, int MAXW>
-__global__ void __launch_bounds__(NT) conv_step_kernel(const Conv a, const long long total, const int nv) {
-  const long long i = (long long)blockIdx.x * NT + threadIdx.x;
+__global__ void __launch_bounds__(NT) conv_step_kernel(const Conv a, const unsigned total, const unsigned nv) {   // total at most 2^31
+  let_next_start();
+  after_previous();                                 // as the scan's step: begins while the kernel before it drains
+  const unsigned i = blockIdx.x * NT + threadIdx.x;
   if (i >= total) return;
-  const int c = (int)(i % nv) * V;
-  const long long bh = i / nv;
-  const int h = (int)(bh % a.H), b = (int)(bh / a.H), w = a.w, d = a.d;
-  T *hist = static_cast<T *>(a.tail) + bh * (w - 1) * d + c;
+  const unsigned bh = i / nv;
+  const int c = (int)(i - bh * nv) * V, b = (int)(bh / (unsigned)a.H), h = (int)(bh - (unsigned)b * a.H), w = a.w, d = a.d;
+  T *hist = static_cast<T *>(a.tail) + (long long)bh * (w - 1) * d + c;
   Vec<T, V> raw[MAXW];                              // raw[j]: the row j tokens back
   raw[0] = load_if<T, V>(static_cast<const T *>(a.x) + b * a.sx.b + h * a.sx.h + c, true);
 #pragma unroll
   for (int j = 1; j < MAXW; ++j) raw[j] = load_if<T, V>(hist + (long long)(w - 1 - j) * d, j < w);
-  const float *fp = a.filt + ((long long)h * d + c) * w;
-  Row<V> o;
+  Pairs<V> f[MAXW], p, q;
+  taps_of<V, MAXW>(f, p, a, (long long)h * d + c, true);
 #pragma unroll
-  for (int e = 0; e < V; ++e) {
-    float p = a.bias ? a.bias[(long long)h * d + c + e] : 0.f;
+  for (int j = 0; j < MAXW; ++j)
+    if (j < w) {
+      to_pairs<V>(q, raw[j]);
 #pragma unroll
-    for (int j = 0; j < MAXW; ++j)
-      if (j < w) p = fmaf(fp[e * w + j], get(raw[j], e), p);
-    put(o, e, a.silu ? silu(p) : p);
-  }
-  store(static_cast<T *>(a.y) + b * a.sy.b + h * a.sy.h + c, o);
+      for (int e = 0; e < (V + 1) / 2; ++e) p[e] = fma(f[j][e], q[e], p[e]);
+    }
+  if (a.silu)
+#pragma unroll
+    for (int e = 0; e < (V + 1) / 2; ++e) p[e] = silu(p[e]);
+  store_pairs<T, V>(static_cast<T *>(a.y) + b * a.sy.b + h * a.sy.h + c, p);
 #pragma unroll
   for (int j = 0; j < MAXW - 1; ++j)
     if (j < w - 1) store(hist + (long long)(w - 2 - j) * d, raw[j]);
@@ -492,8 +495,7 @@ cudaError_t conv_step_launch(const Conv &c, cudaStream_t st) {
   auto go = [&](auto kern, int V) {
     const long long total = (long long)c.B * c.H * (c.d / V), grid = (total + NT - 1) / NT;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-    kern<<<(unsigned)grid, NT, 0, st>>>(c, total, c.d / V);
-    return cudaGetLastError();
+    return launch_next(kern, dim3((unsigned)grid), NT, 0, st, c, (unsigned)total, (unsigned)(c.d / V));
   };
   if (c.bf16) {
     if (v4) return c.w <= 4 ? go(conv_step_kernel<bf16, 4, 4>, 4) : go(conv_step_kernel<bf16, 4, 8>, 4);

@@ -360,82 +360,119 @@ cudaError_t dispatch(const Scan &c, cudaStream_t st) {
   }
 }
 
-// One token per sequence: a lane holds 4 states of one channel, read and
-// written once (16 bytes each when N is a multiple of 4).
+// One token per sequence: a lane holds 4 states of each of two neighbouring
+// channels, read and written once (16 bytes each when N is a multiple of 4 and
+// B, C and the states are aligned for it). Bound by latency: all loads of both
+// channels are on their way together. Launched so that it may begin while the
+// kernel before it drains.
 template <typename T, int NL, bool VEC>
-__global__ void __launch_bounds__(256) scan_step_kernel(const Scan a, const long long channels) {
+__global__ void __launch_bounds__(256) scan_step_kernel(const Scan a, const unsigned units, const unsigned row) {
+  constexpr int U = 2;
+  let_next_start();
+  after_previous();
   const int nl = threadIdx.x % NL, n0 = nl * SPL, N = a.N;
-  const long long chan = ((long long)blockIdx.x * 256 + threadIdx.x) / NL;
-  const bool in = chan < channels;
-  const long long cc = in ? chan : channels - 1;          // spare lanes take part in the shuffles only
-  const int c = (int)(cc % a.d);
-  const long long bh = cc / a.d;
-  const int h = (int)(bh % a.H), b = (int)(bh / a.H), g = h / (a.H / a.G);
+  const unsigned unit = (unsigned)(((unsigned long long)blockIdx.x * 256 + threadIdx.x) / NL);
+  const bool mine = unit < units;
+  const unsigned at = mine ? unit : units - 1;            // spare lanes take part in the shuffles only
+  const unsigned bh = at / row;                           // row = channel pairs of a head
+  const int c = 2 * (int)(at - bh * row), b = (int)(bh / (unsigned)a.H), h = (int)(bh - (unsigned)b * a.H);
+  const int g = h / (a.H / a.G);
+  const bool in[U] = {mine, mine && c + 1 < a.d};
   const long long ch = (long long)h * a.d + c;
-  float *hp = a.state_end + cc * N + n0;
+  float *hp = a.state_end + ((long long)bh * a.d + c) * N + n0;
   const float *Ap = a.A + ch * N + n0;
-  float hs[SPL], A[SPL];
-  if (VEC) {
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f), q = v;
-    if (n0 < N) {
-      v = *reinterpret_cast<const float4 *>(hp);
-      q = *reinterpret_cast<const float4 *>(Ap);
+  const T *Bp = static_cast<const T *>(a.Bm) + b * a.sB.b + g * a.sB.h + n0;
+  const T *Cp = static_cast<const T *>(a.Cm) + b * a.sC.b + g * a.sC.h + n0;
+  const T *xp = static_cast<const T *>(a.x) + b * a.sx.b + h * a.sx.h + c;
+  const T *dp = static_cast<const T *>(a.dt) + b * a.sdt.b + h * a.sdt.h + c;
+  const T *zp = a.z ? static_cast<const T *>(a.z) + b * a.sz.b + h * a.sz.h + c : nullptr;
+  float hs[U][SPL], A[U][SPL], Bv[SPL], Cv[SPL], x[U], dt[U], z[U], D[U], bias[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (VEC) {
+      const Vec<float, 4> v = load_if<float, 4>(hp + u * N, in[u] && n0 < N), q = load_if<float, 4>(Ap + u * N, in[u] && n0 < N);
+#pragma unroll
+      for (int s = 0; s < SPL; ++s) {
+        hs[u][s] = v.e[s];
+        A[u][s] = q.e[s];
+      }
+    } else {
+#pragma unroll
+      for (int s = 0; s < SPL; ++s) {
+        const bool live = in[u] && n0 + s < N;
+        hs[u][s] = live ? hp[u * N + s] : 0.f;
+        A[u][s] = live ? Ap[u * N + s] : 0.f;
+      }
     }
-    hs[0] = v.x, hs[1] = v.y, hs[2] = v.z, hs[3] = v.w;
-    A[0] = q.x, A[1] = q.y, A[2] = q.z, A[3] = q.w;
+    x[u] = in[u] ? to_f(xp[u]) : 0.f;
+    dt[u] = in[u] ? to_f(dp[u]) : 0.f;
+    z[u] = in[u] && zp ? to_f(zp[u]) : 0.f;
+    bias[u] = in[u] && a.dt_bias ? a.dt_bias[ch + u] : 0.f;
+    D[u] = in[u] && a.D ? a.D[ch + u] : 0.f;
+  }
+  if (VEC) {
+    const Vec<T, 4> vb = load_if<T, 4>(Bp, n0 < N), vc = load_if<T, 4>(Cp, n0 < N);
+#pragma unroll
+    for (int s = 0; s < SPL; ++s) {
+      Bv[s] = get(vb, s);
+      Cv[s] = get(vc, s);
+    }
   } else {
 #pragma unroll
     for (int s = 0; s < SPL; ++s) {
-      hs[s] = n0 + s < N ? hp[s] : 0.f;
-      A[s] = n0 + s < N ? Ap[s] : 0.f;
+      Bv[s] = n0 + s < N ? to_f(Bp[s]) : 0.f;
+      Cv[s] = n0 + s < N ? to_f(Cp[s]) : 0.f;
     }
   }
-  const float x = to_f(static_cast<const T *>(a.x)[b * a.sx.b + h * a.sx.h + c]);
-  float e = to_f(static_cast<const T *>(a.dt)[b * a.sdt.b + h * a.sdt.h + c]) + (a.dt_bias ? a.dt_bias[ch] : 0.f);
+  F2 e = pair(dt[0] + bias[0], dt[1] + bias[1]);
   if (a.softplus) e = softplus(e);
-  const T *Bp = static_cast<const T *>(a.Bm) + b * a.sB.b + g * a.sB.h + n0;
-  const T *Cp = static_cast<const T *>(a.Cm) + b * a.sC.b + g * a.sC.h + n0;
-  float y = 0.f;
+  const F2 uu = mul(e, pair(x[0], x[1]));
+  F2 y = both(0.f), h2[SPL];
 #pragma unroll
   for (int s = 0; s < SPL; ++s) {
-    const bool live = n0 + s < N;
-    hs[s] = fmaf(ex2(e * rate(A[s])), hs[s], e * x * (live ? to_f(Bp[s]) : 0.f));
-    y = fmaf(live ? to_f(Cp[s]) : 0.f, hs[s], y);
+    h2[s] = fma(ex2(mul(e, pair(rate(A[0][s]), rate(A[1][s])))), pair(hs[0][s], hs[1][s]), mul(uu, both(Bv[s])));
+    y = fma(both(Cv[s]), h2[s], y);
+    unpair(hs[0][s], hs[1][s], h2[s]);
   }
+  float yv[U];
+  unpair(yv[0], yv[1], y);
 #pragma unroll
-  for (int o = 1; o < NL; o *= 2) y += __shfl_xor_sync(0xffffffffu, y, o);
-  if (!in) return;
-  if (VEC) {
-    if (n0 < N) *reinterpret_cast<float4 *>(hp) = make_float4(hs[0], hs[1], hs[2], hs[3]);
-  } else {
+  for (int u = 0; u < U; ++u) {
 #pragma unroll
-    for (int s = 0; s < SPL; ++s)
-      if (n0 + s < N) hp[s] = hs[s];
-  }
-  if (nl == 0) {
-    if (a.D) y = fmaf(a.D[ch], x, y);
-    if (a.z) y *= silu(to_f(static_cast<const T *>(a.z)[b * a.sz.b + h * a.sz.h + c]));
-    Row<1> o;
-    put(o, 0, y);
-    store(static_cast<T *>(a.y) + b * a.sy.b + h * a.sy.h + c, o);
+    for (int o = 1; o < NL; o *= 2) yv[u] += __shfl_xor_sync(0xffffffffu, yv[u], o);
+    if (!in[u]) continue;
+    if (VEC) {
+      if (n0 < N) sts<SPL>(hp + u * N, hs[u]);
+    } else {
+#pragma unroll
+      for (int s = 0; s < SPL; ++s)
+        if (n0 + s < N) hp[u * N + s] = hs[u][s];
+    }
+    if (nl == u % NL) {                                   // the two channels' ends on two lanes
+      float v = fmaf(D[u], x[u], yv[u]);
+      if (a.z) v *= silu(z[u]);
+      Row<1> o;
+      put(o, 0, v);
+      store(static_cast<T *>(a.y) + b * a.sy.b + h * a.sy.h + c + u, o);
+    }
   }
 }
 
 template <typename T, bool VEC>
 cudaError_t step(const Scan &c, cudaStream_t st) {
-  const long long channels = (long long)c.B * c.H * c.d;
+  const unsigned row = (unsigned)(c.d + 1) / 2;
+  const long long units = (long long)c.B * c.H * row;     // at most 2^31
   const int NL = lanes_of(c.N);
-  const long long grid = (channels * NL + 255) / 256;
+  const long long grid = (units * NL + 255) / 256;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-  auto go = [&](auto kern) { kern<<<(unsigned)grid, 256, 0, st>>>(c, channels); };
+  auto go = [&](auto kern) { return launch_next(kern, dim3((unsigned)grid), 256, 0, st, c, (unsigned)units, row); };
   switch (NL) {
-    case 2: go(scan_step_kernel<T, 2, VEC>); break;
-    case 4: go(scan_step_kernel<T, 4, VEC>); break;
-    case 8: go(scan_step_kernel<T, 8, VEC>); break;
-    case 16: go(scan_step_kernel<T, 16, VEC>); break;
-    default: go(scan_step_kernel<T, 32, VEC>); break;
+    case 2: return go(scan_step_kernel<T, 2, VEC>);
+    case 4: return go(scan_step_kernel<T, 4, VEC>);
+    case 8: return go(scan_step_kernel<T, 8, VEC>);
+    case 16: return go(scan_step_kernel<T, 16, VEC>);
+    default: return go(scan_step_kernel<T, 32, VEC>);
   }
-  return cudaGetLastError();
 }
 
 template <int NL>
@@ -467,8 +504,9 @@ cudaError_t scan_launch(Scan c, cudaStream_t st) {
 }
 
 cudaError_t scan_step_launch(const Scan &c, cudaStream_t st) {
-  const bool vec = c.N % 4 == 0 && reinterpret_cast<uintptr_t>(c.state_end) % 16 == 0 &&
-                   reinterpret_cast<uintptr_t>(c.A) % 16 == 0;
+  const int el = c.bf16 ? 2 : 4;
+  const bool vec = reinterpret_cast<uintptr_t>(c.state_end) % 16 == 0 && reinterpret_cast<uintptr_t>(c.A) % 16 == 0 &&
+                   fits(c.Bm, c.sB, c.N, 4, el) && fits(c.Cm, c.sC, c.N, 4, el);
   if (c.bf16) return vec ? step<bf16, true>(c, st) : step<bf16, false>(c, st);
   return vec ? step<float, true>(c, st) : step<float, false>(c, st);
 }
