@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(32 * W, (NL >= 16 ? 8 : 16) / W) scan_kernel(c
         }
 #pragma unroll
         for (int s = 0; s < SPL; ++s) {
-          hs[c][s] = fma(ex2(mul(ee, A2[c][s])), hs[c][s], mul(uu, pair(B[2 * s], B[2 * s + 1])));
+          hs[c][s] = fma(decay(ee, A2[c][s]), hs[c][s], mul(uu, pair(B[2 * s], B[2 * s + 1])));
           if (!LOCAL) {
             const F2 CC = pair(C[2 * s], C[2 * s + 1]);
             y[c] = s ? fma(CC, hs[c][s], y[c]) : mul(CC, hs[c][s]);
@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const Scan a, const unsi
   F2 y = both(0.f), h2[SPL];
 #pragma unroll
   for (int s = 0; s < SPL; ++s) {
-    h2[s] = fma(ex2(mul(e, pair(rate(A[0][s]), rate(A[1][s])))), pair(hs[0][s], hs[1][s]), mul(uu, both(Bv[s])));
+    h2[s] = fma(decay(e, pair(rate(A[0][s]), rate(A[1][s]))), pair(hs[0][s], hs[1][s]), mul(uu, both(Bv[s])));
     y = fma(both(Cv[s]), h2[s], y);
     unpair(hs[0][s], hs[1][s], h2[s]);
   }

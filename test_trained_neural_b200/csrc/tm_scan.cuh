@@ -69,6 +69,17 @@ __device__ __forceinline__ float rate(float A) {
   return isinf(r) ? copysignf(3.e38f, r) : r;
 }
 
+// exp(e A) = 2^(e rate). The special-function unit's 2^x leans low by 1.5e-8 of
+// the result on average for x in (-1/4, 0) (measured over 4 million arguments;
+// rms 3.4e-8): over a memory of a thousand tokens that would add up to 1.5e-5,
+// while errors of either sign do not. The argument is moved by 2.2e-8 = 1.5e-8
+// log2(e) for it, which the fma does at no cost; 2^2.2e-8 is 1 in fp32, so e = 0
+// leaves a state as it is. It halves the gradients' distance from 64 bits (dA
+// at 4 x 8 x 8192 x 64: 1.8e-6 to 0.9e-6).
+constexpr float kLean = 2.2e-8f;
+__device__ __forceinline__ float decay(float e, float rate) { return ex2(fmaf(e, rate, kLean)); }
+__device__ __forceinline__ F2 decay(F2 e, F2 rate) { return ex2(fma(e, rate, both(kLean))); }
+
 // Lanes that share a channel for N states.
 inline int lanes_of(int N) {
   int nl = 2;
@@ -122,7 +133,7 @@ static __global__ void __launch_bounds__(128) join_segments_kernel(const Scan a,
     for (int k = 0; k < U; ++k) {
       const long long q = back ? S - 1 - (k0 + k) : 1 + k0 + k;
       if (k0 + k >= steps) break;
-      v = fmaf(ex2(A2 * e[k]), v, l[k]);
+      v = fmaf(decay(e[k], A2), v, l[k]);
       p[q * per * NP] = v;
     }
   }

@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) states_kernel(const Scan a, co
         if (SPLIT) es = add(es, ee);
 #pragma unroll
         for (int s = 0; s < SPL; ++s) {
-          const F2 av = ex2(mul(ee, A2[s]));
+          const F2 av = decay(ee, A2[s]);
           hs[s] = fma(av, hs[s], mul(uu, pair(B[2 * s], B[2 * s + 1])));
           if (SPLIT) {
             Pr[s] = mul(Pr[s], av);
@@ -534,7 +534,7 @@ __global__ void __launch_bounds__(32 * W, 12 / W) grad_kernel(const Scan a, cons
 #pragma unroll
         for (int s = 0; s < SPL; ++s) {
           h0[s] = pair(q0[s], q1[s]);
-          if (SPLIT && w.seg > 0) h0[s] = fma(ex2(mul(A2[s], cum[q])), hin[s], h0[s]);
+          if (SPLIT && w.seg > 0) h0[s] = fma(decay(cum[q], A2[s]), hin[s], h0[s]);
         }
         // the chunk's decays and states again
         F2 hv[K][SPL];
@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(32 * W, 12 / W) grad_kernel(const Scan a, cons
           const F2 ee = pair(e[0], e[1]), uu = pair(u[0], u[1]);
 #pragma unroll
           for (int s = 0; s < SPL; ++s) {
-            hv[i][s] = fma(ex2(mul(ee, A2[s])), i ? hv[i ? i - 1 : 0][s] : h0[s], mul(uu, pair(B[2 * s], B[2 * s + 1])));
+            hv[i][s] = fma(decay(ee, A2[s]), i ? hv[i ? i - 1 : 0][s] : h0[s], mul(uu, pair(B[2 * s], B[2 * s + 1])));
           }
         }
 #pragma unroll
@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(32 * W, 12 / W) grad_kernel(const Scan a, cons
             dC[s] = lo + hi;
             unpair(lo, hi, mul(g, uu));
             dB[s] = lo + hi;
-            R[s] = mul(g, ex2_again(mul(ee, A2[s])));
+            R[s] = mul(g, ex2_again(fma(ee, A2[s], both(kLean))));
             const F2 qq = mul(R[s], hp);
             dA[s] = fma(qq, ee, dA[s]);
             un = s ? fma(g, BB, un) : mul(g, BB);

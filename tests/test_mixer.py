@@ -339,6 +339,22 @@ def test_scan_decay_of_the_lowest_values(T):
         assert torch.isfinite(g[k]).all(), k
 
 
+@pytest.mark.parametrize("T", [1, 40, 3000])
+def test_tokens_that_write_nothing_leave_the_state_bit_for_bit(T):
+    """e = softplus(-200 ...) = 0: exp(e A) is 1 exactly, however often, in prompts, split prompts and steps."""
+    r, c, o = scan_case(2, 2, 1, T, 16, 16, F)
+    c["dt"].fill_(-200.0)
+    _, end = tm.selective_scan(**c, **o)
+    assert torch.equal(end, o["state"])
+    state = o["state"].clone()
+    tm.selective_scan_step(c["x"][:, :, 0], c["dt"][:, :, 0], c["A"], c["Bm"][:, :, 0], c["Cm"][:, :, 0], state,
+                           dt_bias=o["dt_bias"])
+    assert torch.equal(state, o["state"])
+    ds = r.normal(2, 2, 16, 16)
+    g = tm.selective_scan_backward(**c, dy=torch.zeros_like(c["x"]), **o, dstate_end=ds)
+    assert torch.equal(g["dstate"], ds)
+
+
 def test_expanded_inputs():
     """x itself repeated over the batch: outputs are whole tensors of their own."""
     r = Draw("expand")
