@@ -127,17 +127,18 @@ __device__ __forceinline__ void sts(float *p, const float (&v)[V]) {
 }
 
 // Asynchronous copy of V elements into shared memory, zeros where not `live`
-// (nothing is read then, so src may point anywhere). Pieces under 4 bytes have no asynchronous form and
-// are copied at once. A thread that reads only what it copied itself needs
-// copies_done() and no barrier.
+// (nothing is read then, so src may point anywhere). Pieces under 4 bytes have
+// no asynchronous form and are copied at once. A thread that reads only what it
+// copied itself needs copies_done() and no barrier; its earlier reads of a slot
+// stay before the copy into it.
 template <typename T, int V>
 __device__ __forceinline__ void copy_in(T *dst, const T *src, bool live) {
   constexpr int n = sizeof(T) * V;
   if constexpr (n >= 4) {
     const unsigned d = (unsigned)__cvta_generic_to_shared(dst);
     const int k = live ? n : 0;
-    if constexpr (n == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(k));
-    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(d), "l"(src), "n"(n), "r"(k));
+    if constexpr (n == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(k) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(d), "l"(src), "n"(n), "r"(k) : "memory");
   } else {
     store(dst, load_if<T, V>(src, live));
   }
@@ -171,7 +172,6 @@ __device__ __forceinline__ F2 ex2(F2 x) {
   unpair(a, b, x);
   return pair(ex2(a), ex2(b));
 }
-
 __device__ __forceinline__ F2 add(F2 a, F2 b) {
   F2 r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
@@ -293,7 +293,7 @@ __device__ __forceinline__ F2 silu_grad(F2 p) {
   return mul(q, fma(p, fma(q, both(-1.f), one), one));
 }
 __device__ __forceinline__ F2 keep_if(F2 x, bool live) { return live ? x : both(0.f); }
-// ex2 whose value the compiler may not keep from an earlier one.
+// 2^x whose value the compiler may not keep from an earlier one.
 __device__ __forceinline__ F2 ex2_again(F2 x) {
   float a, b;
   unpair(a, b, x);

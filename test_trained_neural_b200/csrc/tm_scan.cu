@@ -1,7 +1,6 @@
 // Selective state-space scan: prompts (with the sequence split over CTAs when
 // there are few channels) and single tokens. Formulas and lane layout:
 // tm_scan.cuh.
-#include <cstdlib>
 #include "tm_scan.cuh"
 
 namespace tmem {
@@ -302,7 +301,7 @@ Plan plan_of(int B, int H, int T, int d) {
   p.warps = d <= 2 * CW ? 2 : 4;
   p.blocks = (d + CW * p.warps - 1) / (CW * p.warps);
   const long long warps = (long long)B * H * ((d + CW - 1) / CW);
-  const long long want = (long long)kSMs * (getenv("TMW") ? atoi(getenv("TMW")) : 16);
+  const long long want = (long long)kSMs * 16;
   long long S = want / warps;
   const long long most = T / 32;                   // at least 32 tokens a segment
   if (S > most) S = most;
