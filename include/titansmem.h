@@ -357,8 +357,9 @@ TM_API tm_status tm_prologue(int B, int H, int T, int d, int width, tm_dtype in_
  *    histories and statistics are contiguous.
  *  - lengths: NULL, or device [B] int32, the tokens of each sequence of a padded
  *    batch (values outside [0, T] are held to it). Rows behind a sequence's end
- *    are not read; outputs there are left as they were, gradients of tokens
- *    there are written as zeros. A sequence of length 0 is allowed.
+ *    are not read; outputs there are left as they were, or written as zeros when
+ *    the call's zero_behind is not 0; gradients of tokens there are always
+ *    written as zeros. A sequence of length 0 is allowed.
  *  - Pointers are aligned to their elements (workspaces to 256 bytes); wide
  *    loads are used where bases, strides and sizes allow. d need not be a
  *    multiple of anything.
@@ -388,8 +389,8 @@ TM_API tm_status tm_prologue(int B, int H, int T, int d, int width, tm_dtype in_
  *   tail       [B, H, width-1, d] dtype or NULL, output: the last width-1 tokens
  *              of hist and x (of each sequence's own length): the next call's hist
  */
-TM_API tm_status tm_conv(int B, int H, int T, int d, int width, tm_dtype dtype, tm_act act, const void *x,
-                         const float *filt, const float *bias, const void *hist, const int *lengths, void *y,
+TM_API tm_status tm_conv(int B, int H, int T, int d, int width, tm_dtype dtype, tm_act act, int zero_behind,
+                         const void *x, const float *filt, const float *bias, const void *hist, const int *lengths, void *y,
                          void *tail, const long long *strides, void *stream);
 
 /*
@@ -430,8 +431,8 @@ TM_API tm_status tm_conv_step(int B, int H, int d, int width, tm_dtype dtype, tm
  * may then be NULL).
  */
 TM_API tm_status tm_scan_workspace_size(int B, int H, int G, int T, int d, int N, tm_dtype dtype, size_t *bytes);
-TM_API tm_status tm_scan(int B, int H, int G, int T, int d, int N, tm_dtype dtype, int dt_softplus, const void *x,
-                         const void *dt, const float *A, const void *Bm, const void *Cm, const float *D, const void *z,
+TM_API tm_status tm_scan(int B, int H, int G, int T, int d, int N, tm_dtype dtype, int dt_softplus, int zero_behind,
+                         const void *x, const void *dt, const float *A, const void *Bm, const void *Cm, const float *D, const void *z,
                          const float *dt_bias, const float *state0, const int *lengths, void *y, float *state_end,
                          const long long *strides, void *workspace, size_t workspace_bytes, void *stream);
 
@@ -478,14 +479,14 @@ TM_API tm_status tm_scan_step(int B, int H, int G, int d, int N, tm_dtype dtype,
  *   weight, bias [H, d] or NULL (= 1, 0)
  *   stats [B, H, T, 2] (TM_NORM_TOKEN) or [B, H, 2], or NULL, output: mean and
  *         1 / sqrt(var + eps) for the backward; zeros for an empty sequence, rows
- *         behind a sequence's end left as they were; 8-byte aligned
+ *         behind a sequence's end as in y; 8-byte aligned
  *   workspace: tm_group_norm_workspace_size(..., backward = 0) bytes (may be 0)
  */
 typedef enum { TM_NORM_TOKEN = 0, TM_NORM_SEQUENCE = 1 } tm_norm_over;
 TM_API tm_status tm_group_norm_workspace_size(int B, int H, int T, int d, tm_norm_over over, int backward,
                                               size_t *bytes);
 TM_API tm_status tm_group_norm(int B, int H, int T, int d, tm_norm_over over, tm_dtype in_dtype, tm_dtype out_dtype,
-                               tm_act act, float eps, const void *x, const float *weight, const float *bias,
+                               tm_act act, int zero_behind, float eps, const void *x, const float *weight, const float *bias,
                                const int *lengths, void *y, float *stats, const long long *strides, void *workspace,
                                size_t workspace_bytes, void *stream);
 

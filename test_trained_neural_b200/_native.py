@@ -39,17 +39,17 @@ SIGNATURES = {
     "tm_decode_step": (_I, [_P, _I, _I, _I] + [_P] * 9 + [_P]),
     "tm_backward_workspace_size": (_I, [_P, _I, _I, _I, _I, _I, ctypes.POINTER(ctypes.c_size_t)]),
     "tm_backward": (_I, [_P, _I, _I, _I, _I, _I] + [_P] * 20 + [ctypes.c_size_t, _P]),
-    "tm_conv": (_I, [_I] * 7 + [_P] * 7 + [_P, _P]),
+    "tm_conv": (_I, [_I] * 8 + [_P] * 7 + [_P, _P]),
     "tm_conv_backward_workspace_size": (_I, [_I] * 6 + [ctypes.POINTER(_SZ)]),
     "tm_conv_backward": (_I, [_I] * 7 + [_P] * 11 + [_P, _P, _SZ, _P]),
     "tm_conv_step": (_I, [_I] * 6 + [_P] * 5 + [_P, _P]),
     "tm_scan_workspace_size": (_I, [_I] * 7 + [ctypes.POINTER(_SZ)]),
-    "tm_scan": (_I, [_I] * 8 + [_P] * 12 + [_P, _P, _SZ, _P]),
+    "tm_scan": (_I, [_I] * 9 + [_P] * 12 + [_P, _P, _SZ, _P]),
     "tm_scan_backward_workspace_size": (_I, [_I] * 7 + [ctypes.POINTER(_SZ)]),
     "tm_scan_backward": (_I, [_I] * 8 + [_P] * 21 + [_P, _P, _SZ, _P]),
     "tm_scan_step": (_I, [_I] * 7 + [_P] * 10 + [_P, _P]),
     "tm_group_norm_workspace_size": (_I, [_I] * 6 + [ctypes.POINTER(_SZ)]),
-    "tm_group_norm": (_I, [_I] * 8 + [_F] + [_P] * 6 + [_P, _P, _SZ, _P]),
+    "tm_group_norm": (_I, [_I] * 9 + [_F] + [_P] * 6 + [_P, _P, _SZ, _P]),
     "tm_group_norm_backward": (_I, [_I] * 8 + [_P] * 9 + [_P, _P, _SZ, _P]),
     "tm_status_string": (ctypes.c_char_p, [_I]),
     "tm_version": (_I, []),

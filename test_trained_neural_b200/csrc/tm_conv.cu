@@ -112,6 +112,14 @@ __global__ void __launch_bounds__(NT, 2) conv_kernel(const Conv a, const Split s
   const T *hist = a.hist ? static_cast<const T *>(a.hist) + ((long long)b * a.H + h) * (w - 1) * d + c : nullptr;
   const long long t0 = ((long long)tile * sp.RL + rl) * run;
   const long long t1 = t0 + run < n ? t0 + run : n;
+  if (a.zero_rest) {
+    T *y = static_cast<T *>(a.y) + b * a.sy.b + h * a.sy.h + c;
+    const long long last = t0 + run < a.T ? t0 + run : a.T;
+    Row<V> o;
+#pragma unroll
+    for (int e = 0; e < V; ++e) put(o, e, 0.f);
+    for (long long t = t0 > n ? t0 : n; t < last; ++t) store(y + t * a.sy.t, o);
+  }
 
   // the tail: rows n - (w - 1) .. n - 1 of history and tokens
   if (a.tail && tile == 0) {

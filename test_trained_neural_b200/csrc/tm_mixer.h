@@ -17,7 +17,7 @@ enum Over { kToken = 0, kSequence = 1 };
 
 struct Conv {
   int B, H, T, d, w;
-  bool bf16, silu;
+  bool bf16, silu, zero_rest;        // zero_rest: rows behind a sequence's end of y are written as zeros
   const void *x, *hist, *dy, *dtail;
   const float *filt, *bias;
   const int *lengths;
@@ -33,7 +33,7 @@ size_t conv_backward_ws(int B, int H, int T, int d, int w);
 
 struct Scan {
   int B, H, G, T, d, N;
-  bool bf16, softplus;
+  bool bf16, softplus, zero_rest;
   const void *x, *dt, *Bm, *Cm, *z, *dy;
   const float *A, *D, *dt_bias, *state0, *dstate_end;
   const int *lengths;
@@ -51,7 +51,7 @@ size_t scan_backward_ws(int B, int H, int G, int T, int d, int N);
 struct Norm {
   int B, H, T, d;
   Over over;
-  bool silu, in_bf16, out_bf16;
+  bool silu, in_bf16, out_bf16, zero_rest;
   float eps;
   const void *x, *dy;
   const float *weight, *bias;

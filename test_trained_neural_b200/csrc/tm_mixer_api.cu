@@ -98,8 +98,8 @@ extern "C" {
 
 // ---- short convolution
 
-tm_status tm_conv(int B, int H, int T, int d, int width, tm_dtype dtype, tm_act act, const void *x, const float *filt,
-                  const float *bias, const void *hist, const int *lengths, void *y, void *tail,
+tm_status tm_conv(int B, int H, int T, int d, int width, tm_dtype dtype, tm_act act, int zero_behind, const void *x,
+                  const float *filt, const float *bias, const void *hist, const int *lengths, void *y, void *tail,
                   const long long *strides, void *stream) {
   if (!sizes_ok(B, H, T, d, dtype) || width < 1 || width > 8 || !act_ok(act)) return TM_ERR_INVALID_ARG;
   if (!x || !filt || !y) return TM_ERR_INVALID_ARG;
@@ -118,7 +118,7 @@ tm_status tm_conv(int B, int H, int T, int d, int width, tm_dtype dtype, tm_act 
   c.B = B, c.H = H, c.T = T, c.d = d, c.w = width;
   c.bf16 = dtype == TM_BF16, c.silu = act == TM_ACT_SILU;
   c.x = x, c.filt = filt, c.bias = bias, c.hist = width > 1 ? hist : nullptr, c.lengths = lengths;
-  c.y = y, c.tail = width > 1 ? tail : nullptr;
+  c.y = y, c.tail = width > 1 ? tail : nullptr, c.zero_rest = zero_behind && lengths;
   return done(tmem::mix::conv_launch(c, cs(stream)));
 }
 
@@ -192,7 +192,7 @@ tm_status tm_scan_workspace_size(int B, int H, int G, int T, int d, int N, tm_dt
   return TM_OK;
 }
 
-tm_status tm_scan(int B, int H, int G, int T, int d, int N, tm_dtype dtype, int dt_softplus, const void *x,
+tm_status tm_scan(int B, int H, int G, int T, int d, int N, tm_dtype dtype, int dt_softplus, int zero_behind, const void *x,
                   const void *dt, const float *A, const void *Bm, const void *Cm, const float *D, const void *z,
                   const float *dt_bias, const float *state0, const int *lengths, void *y, float *state_end,
                   const long long *strides, void *workspace, size_t workspace_bytes, void *stream) {
@@ -226,7 +226,7 @@ tm_status tm_scan(int B, int H, int G, int T, int d, int N, tm_dtype dtype, int 
   c.B = B, c.H = H, c.G = G, c.T = T, c.d = d, c.N = N;
   c.bf16 = dtype == TM_BF16, c.softplus = dt_softplus != 0;
   c.x = x, c.dt = dt, c.Bm = Bm, c.Cm = Cm, c.z = z, c.A = A, c.D = D, c.dt_bias = dt_bias, c.state0 = state0;
-  c.lengths = lengths, c.y = y, c.state_end = state_end, c.ws = workspace;
+  c.lengths = lengths, c.y = y, c.state_end = state_end, c.ws = workspace, c.zero_rest = zero_behind && lengths;
   return done(tmem::mix::scan_launch(c, cs(stream)));
 }
 
@@ -329,7 +329,7 @@ tm_status tm_group_norm_workspace_size(int B, int H, int T, int d, tm_norm_over 
 }
 
 tm_status tm_group_norm(int B, int H, int T, int d, tm_norm_over over, tm_dtype in_dtype, tm_dtype out_dtype,
-                        tm_act act, float eps, const void *x, const float *weight, const float *bias,
+                        tm_act act, int zero_behind, float eps, const void *x, const float *weight, const float *bias,
                         const int *lengths, void *y, float *stats, const long long *strides, void *workspace,
                         size_t workspace_bytes, void *stream) {
   if (!norm_sizes_ok(B, H, T, d, over, in_dtype, out_dtype) || !act_ok(act) || !(eps >= 0.f)) return TM_ERR_INVALID_ARG;
@@ -352,6 +352,7 @@ tm_status tm_group_norm(int B, int H, int T, int d, tm_norm_over over, tm_dtype 
   c.B = B, c.H = H, c.T = T, c.d = d, c.over = over_of(over), c.silu = act == TM_ACT_SILU;
   c.in_bf16 = in_dtype == TM_BF16, c.out_bf16 = out_dtype == TM_BF16, c.eps = eps;
   c.x = x, c.weight = weight, c.bias = bias, c.lengths = lengths, c.y = y, c.stats = stats, c.ws = workspace;
+  c.zero_rest = zero_behind && lengths;
   return done(tmem::mix::norm_launch(c, cs(stream)));
 }
 

@@ -73,6 +73,21 @@ __device__ __forceinline__ void affine_of(Pairs<V> &w, Pairs<V> &bs, const Norm 
   if (live && a.bias) lds<V>(bs, a.bias + hc);
 }
 
+// Zeros for the rows of y from the sequence's end on (and their statistics,
+// token by token): rows first, first + step, ... of `width` channels by `lanes` threads.
+template <typename TO>
+__device__ __forceinline__ void zero_rows(const Norm &a, int b, int h, long long first, long long step, int lane, int lanes,
+                                          int width, bool stats) {
+  TO *y = static_cast<TO *>(a.y) + b * a.sy.b + h * a.sy.h;
+  Row<1> o;
+  put(o, 0, 0.f);
+  for (long long t = first; t < a.T; t += step) {
+    for (int c = lane; c < width; c += lanes) store(y + t * a.sy.t + c, o);
+    if (stats && lane == 0)
+      reinterpret_cast<float2 *>(a.stats)[((long long)b * a.H + h) * a.T + t] = make_float2(0.f, 0.f);
+  }
+}
+
 // ---- one token
 
 // CTA: one (batch, head) and the rows tile, tile + tiles, ... in steps of
@@ -149,6 +164,7 @@ __global__ void __launch_bounds__(NT) token_kernel(const Norm a, const int tiles
     }
     y += step * a.sy.t;
   }
+  if (a.zero_rest) zero_rows<TO>(a, b, h, n + (long long)tile * ROWS + rg, (long long)tiles * ROWS, lane, LPR, d, a.stats);
 }
 
 // Rows too long for registers: a CTA per row, which reads it three times (twice from L1 and L2).
@@ -158,7 +174,10 @@ __global__ void __launch_bounds__(NT) token_wide_kernel(const Norm a) {
   const long long row = blockIdx.x;
   const int t = (int)(row % a.T), bh = (int)(row / a.T);
   const int h = bh % a.H, b = bh / a.H, d = a.d;
-  if (t >= tokens_of(a.lengths, b, a.T)) return;
+  if (t >= tokens_of(a.lengths, b, a.T)) {
+    if (a.zero_rest) zero_rows<TO>(a, b, h, t, a.T, threadIdx.x, NT, d, a.stats);
+    return;
+  }
   const TI *x = static_cast<const TI *>(a.x) + b * a.sx.b + h * a.sx.h + t * a.sx.t;
   TO *y = static_cast<TO *>(a.y) + b * a.sy.b + h * a.sy.h + t * a.sy.t;
   float m = 0.f, q = 0.f;
@@ -514,6 +533,13 @@ __global__ void __launch_bounds__(NT) seq_apply_kernel(const Norm a, const Cols 
       }
       if (t + i < t1) store_pairs<TO, V>(y + (t + i) * a.sy.t, u);
     }
+  }
+  if (a.zero_rest) {
+    const long long last = t0 + s.run < a.T ? t0 + s.run : a.T;
+    Row<V> o;
+#pragma unroll
+    for (int e = 0; e < V; ++e) put(o, e, 0.f);
+    for (long long t = t0 > n ? t0 : n; t < last; ++t) store(y + t * a.sy.t, o);
   }
 }
 

@@ -268,6 +268,16 @@ __global__ void __launch_bounds__(32 * W, (NL >= 16 ? 8 : 16) / W) scan_kernel(c
     }
   }
   copies_done();
+  if (!LOCAL && a.zero_rest) {
+    const long long last = t_seg + pl.L < a.T ? t_seg + pl.L : a.T;
+    Row<V> o;
+#pragma unroll
+    for (int i = 0; i < V; ++i) put(o, i, 0.f);
+    for (long long t0 = t_end > t_seg ? t_end : t_seg; t0 < last; t0 += TQ)
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+        if (c_blk + col_at(k) < a.d && t0 + row_at(k) < last) store(yp + (t0 + row_at(k)) * a.sy.t + col_at(k), o);
+  }
 
 #pragma unroll
   for (int c = 0; c < CPL; ++c) {

@@ -738,10 +738,8 @@ __global__ void __launch_bounds__(32 * W, 12 / W) grad_kernel(const Scan a, cons
 
 // dB and dC: the partials of the channel blocks that share them, in order.
 template <typename T>
-__global__ void __launch_bounds__(256) join_bc_kernel(const Scan a, const Plan pl, const float *bc) {
-  let_next_start();
-  after_previous();
-  const long long rows = (long long)a.B * a.G * a.T, i = (long long)blockIdx.x * 256 + threadIdx.x;
+__device__ __forceinline__ void join_bc(const Scan &a, const Plan &pl, const float *bc, unsigned block) {
+  const long long rows = (long long)a.B * a.G * a.T, i = (long long)block * 256 + threadIdx.x;
   const int lg = __ffs(2 * pl.NP) - 1;                  // 2 NP is a power of two
   const long long row = i >> lg;
   if (row >= rows) return;
@@ -755,11 +753,10 @@ __global__ void __launch_bounds__(256) join_bc_kernel(const Scan a, const Plan p
 }
 
 // dA, dD and d(dt_bias): the partials of the sequences and segments, in order.
-__global__ void __launch_bounds__(256) join_param_kernel(const Scan a, const Plan pl, const float *ws) {
+__device__ __forceinline__ void join_params(const Scan &a, const Plan &pl, const float *ws, unsigned block) {
   __shared__ float red[8][32];
-  after_previous();
   const long long HD = (long long)a.H * a.d, nA = HD * pl.NP, n = nA + 2 * HD;
-  const long long i = (long long)blockIdx.x * 32 + threadIdx.x % 32;
+  const long long i = (long long)block * 32 + threadIdx.x % 32;
   const int k = threadIdx.x / 32, parts = a.B * pl.S;
   float s = 0.f;
   if (i < n)
@@ -780,13 +777,22 @@ __global__ void __launch_bounds__(256) join_param_kernel(const Scan a, const Pla
   }
 }
 
+// Both, the first `bc` blocks for dB and dC.
+template <typename T>
+__global__ void __launch_bounds__(256) join_kernel(const Scan a, const Plan pl, const float *ws, const unsigned bc) {
+  after_previous();
+  if (blockIdx.x < bc) join_bc<T>(a, pl, ws + pl.bc, blockIdx.x);
+  else join_params(a, pl, ws, blockIdx.x - bc);
+}
+
 template <typename T, int NL, int VF, int VB, int W, bool SPLIT>
 cudaError_t run(const Scan &c, const Plan &p, cudaStream_t st) {
   constexpr int NP = NL * SPL, thr = 32 * W;
   float *ws = static_cast<float *>(c.ws);
   const long long grid = (long long)c.B * c.H * p.blocks * p.S;
-  const long long nbc = (long long)c.B * c.G * c.T * 2 * NP;
-  if (grid > 0x7fffffffLL || (nbc + 255) / 256 > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const long long bc = p.pbn > 1 ? ((long long)c.B * c.G * c.T * 2 * NP + 255) / 256 : 0;   // blocks of join_kernel
+  const long long params = ((long long)c.H * c.d * (NP + 2) + 31) / 32;
+  if (grid > 0x7fffffffLL || bc + params > 0x7fffffffLL) return cudaErrorInvalidValue;
   cudaError_t e = cudaSuccess;
   constexpr size_t sm1 = StatesSmem<T, NL, VF, W, SPLIT>::bytes;
   auto states = states_kernel<T, NL, VF, W, SPLIT>;
@@ -805,12 +811,7 @@ cudaError_t run(const Scan &c, const Plan &p, cudaStream_t st) {
   }
   e = launch_next(grad, dim3((unsigned)grid), thr, sm2, st, c, p, ws);
   if (e != cudaSuccess) return e;
-  if (p.pbn > 1) {
-    e = launch_next(join_bc_kernel<T>, dim3((unsigned)((nbc + 255) / 256)), 256, 0, st, c, p, ws + p.bc);
-    if (e != cudaSuccess) return e;
-  }
-  const long long n = (long long)c.H * c.d * (NP + 2);
-  return launch_next(join_param_kernel, dim3((unsigned)((n + 31) / 32)), 256, 0, st, c, p, ws);
+  return launch_next(join_kernel<T>, dim3((unsigned)(bc + params)), 256, 0, st, c, p, ws, (unsigned)bc);
 }
 
 template <typename T, int NL, int VF, int VB>

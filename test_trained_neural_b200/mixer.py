@@ -141,11 +141,6 @@ _stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
-def _fresh(like, lengths, dtype=None):
-    """An output: zeros where rows behind a sequence's end are not written."""
-    return torch.empty_like(like, dtype=dtype) if lengths is None else torch.zeros_like(like, dtype=dtype)
-
-
 @functools.lru_cache(maxsize=4096)
 def _workspace_size(fn, *sizes):
     n = ctypes.c_size_t()
@@ -189,11 +184,12 @@ def short_conv(x, filt, bias=None, *, hist=None, lengths=None, act="silu", out=N
     shape = B, H, T, d = _shape("x", x, 4)
     code = _dtype_code("x", x)
     w = _conv_check(x, shape, filt, bias, hist, lengths, out, tail)
-    if out is None:
-        out = _fresh(x, lengths)
+    fresh = out is None                                  # then rows behind the ends are written as zeros
+    if fresh:
+        out = torch.empty_like(x)
     if tail is None:
         tail = x.new_empty((B, H, w - 1, d))
-    N.check(N.load().tm_conv(B, H, T, d, w, code, _named(_ACTS, "act", act), x.data_ptr(), filt.data_ptr(), _p(bias),
+    N.check(N.load().tm_conv(B, H, T, d, w, code, _named(_ACTS, "act", act), fresh, x.data_ptr(), filt.data_ptr(), _p(bias),
                              _p(hist), _p(lengths), out.data_ptr(), tail.data_ptr(), _strides("x out", x, out),
                              _stream_of(x.get_device())), "tm_conv")
     return out, tail
@@ -277,12 +273,13 @@ def selective_scan(x, dt, A, Bm, Cm, *, D=None, z=None, dt_bias=None, state=None
     shape = B, H, T, d = _shape("x", x, 4)
     code = _dtype_code("x", x)
     G, n = _scan_sizes(x, shape, dt, A, Bm, Cm, D, z, dt_bias, state, state_end, out, lengths)
-    if out is None:
-        out = _fresh(x, lengths)
+    fresh = out is None
+    if fresh:
+        out = torch.empty_like(x)
     if state_end is None:
         state_end = A.new_empty((B, H, d, n))
     ws, nb = _workspace(workspace, x, "tm_scan_workspace_size", B, H, G, T, d, n, code)
-    N.check(N.load().tm_scan(B, H, G, T, d, n, code, bool(softplus), x.data_ptr(), dt.data_ptr(), A.data_ptr(),
+    N.check(N.load().tm_scan(B, H, G, T, d, n, code, bool(softplus), fresh, x.data_ptr(), dt.data_ptr(), A.data_ptr(),
                              Bm.data_ptr(), Cm.data_ptr(), _p(D), _p(z), _p(dt_bias), _p(state), _p(lengths),
                              out.data_ptr(), state_end.data_ptr(),
                              _strides("x dt Bm Cm z out", x, dt, Bm, Cm, z, out), _p(ws), nb,
@@ -369,12 +366,14 @@ def group_norm(x, weight=None, bias=None, *, over="token", act=None, eps=1e-5, l
         raise TypeError(f"the output must be float32 or bfloat16, got {kind}")
     code, where = _dtype_code("x", x), _named(_OVER, "over", over)
     kept = _norm_check(x, shape, weight, bias, lengths, stats, over, out, kind)
-    if out is None:
-        out = _fresh(x, lengths, kind)
+    fresh = out is None
+    if fresh:
+        out = torch.empty_like(x, dtype=kind)
     if stats is None:
-        stats = (x.new_empty if lengths is None or over == "sequence" else x.new_zeros)(kept, dtype=_F32)
+        # rows behind the ends: written with those of y, so zeroed here when those of a given y are left alone
+        stats = (x.new_empty if lengths is None or fresh else x.new_zeros)(kept, dtype=_F32)
     ws, n = _workspace(workspace, x, "tm_group_norm_workspace_size", B, H, T, d, where, 0)
-    N.check(N.load().tm_group_norm(B, H, T, d, where, code, _TYPES[kind], _named(_ACTS, "act", act), float(eps),
+    N.check(N.load().tm_group_norm(B, H, T, d, where, code, _TYPES[kind], _named(_ACTS, "act", act), fresh, float(eps),
                                    x.data_ptr(), _p(weight), _p(bias), _p(lengths), out.data_ptr(), stats.data_ptr(),
                                    _strides("x out", x, out), _p(ws), n, _stream_of(x.get_device())), "tm_group_norm")
     return out, stats

@@ -46,7 +46,7 @@ def call(fn, names, sizes, ws=1 << 40, strides=None, eps=None, **change):
 
 
 def conv(B=2, H=2, T=64, d=8, w=4, kind=N.TM_F32, act=0, **k):
-    return call("tm_conv", CONV, (B, H, T, d, w, kind, act), **k)
+    return call("tm_conv", CONV, (B, H, T, d, w, kind, act, 0), **k)
 
 
 def conv_b(B=2, H=2, T=64, d=8, w=4, kind=N.TM_F32, act=0, **k):
@@ -58,7 +58,7 @@ def conv_s(B=2, H=2, d=8, w=4, kind=N.TM_F32, act=0, **k):
 
 
 def scan(B=2, H=2, G=1, T=64, d=8, n=16, kind=N.TM_F32, sp=1, **k):
-    return call("tm_scan", SCAN, (B, H, G, T, d, n, kind, sp), **k)
+    return call("tm_scan", SCAN, (B, H, G, T, d, n, kind, sp, 0), **k)
 
 
 def scan_b(B=2, H=2, G=1, T=64, d=8, n=16, kind=N.TM_F32, sp=1, **k):
@@ -70,7 +70,7 @@ def scan_s(B=2, H=2, G=1, d=8, n=16, kind=N.TM_F32, sp=1, **k):
 
 
 def norm(B=2, H=2, T=64, d=8, over=1, a=N.TM_F32, b=N.TM_F32, act=0, eps=1e-5, **k):
-    return call("tm_group_norm", NORM, (B, H, T, d, over, a, b, act), eps=eps, **k)
+    return call("tm_group_norm", NORM, (B, H, T, d, over, a, b, act, 0), eps=eps, **k)
 
 
 def norm_b(B=2, H=2, T=64, d=8, over=1, a=N.TM_F32, b=N.TM_F32, act=0, **k):
