@@ -17,6 +17,7 @@ NVCC_FLAGS = [
     "-Xcompiler", "-fPIC,-fvisibility=hidden", "-shared",
     "--expt-relaxed-constexpr", "--extended-lambda",
     "-Xptxas", "-v",
+    "--threads", "0",            # the source files side by side
 ]
 
 
