@@ -7,18 +7,20 @@
 //
 // Two passes over the tokens. The first walks forward and keeps the state at
 // every 4th token (fp32). The second walks backward in chunks of 4 tokens: from
-// a kept state it forms the chunk's 4 decays and states again, holds both in
-// registers (2 channels x 4 states x 4 tokens a lane), and takes the chunk's
-// tokens in reverse. exp() is so evaluated twice per (token, channel, state)
-// in all, and no state is read back from memory but the kept ones.
+// a kept state it forms the chunk's 4 states again, holds them in registers (2
+// channels x 4 states x 4 tokens a lane), and takes the chunk's tokens in
+// reverse, evaluating their decays once more. exp() is so evaluated three times
+// per (token, channel, state) in all (the special-function unit has the room),
+// and no state is read back from memory but the kept ones.
 // When there are few channels the sequence is split into segments that both
 // passes take at the same time: the first pass starts each from a zero state
 // and also forms what the segment adds to the gradient that enters it from
-// behind, sum_t (prod a up to t) Cm_t k_t; the second joins the segments before
-// (state) and after (gradient) its own, with the segments' decays exp(A sum e).
+// behind, sum_t (prod a up to t) Cm_t k_t; a launch between the passes joins the
+// segments, states from the front and gradients from the back, with the
+// segments' decays exp(A sum e).
 //
 // Measured on B200, 4 x 8 x 8192 x 64 bf16, 16 states, 13 segments: first pass
-// 142 us, second 376 us, at 11 warps an SM half of the issue slots used, the
+// 142 us, second 376 us: at 11 warps an SM half of the issue slots used, the
 // special-function unit 0.38: the dependent chains of a chunk bound it. Holding
 // the decays of a chunk instead of evaluating them again spills (513 us); chunks
 // of 8 at 8 warps an SM took 609 us; the states in shared memory at 16 warps 407.
