@@ -371,7 +371,8 @@ TM_API tm_status tm_prologue(int B, int H, int T, int d, int width, tm_dtype in_
  *    to one call at a time: calls that may overlap on the GPU, captured graphs
  *    included, need their own.
  *  - Limits: H * d <= 2^24, B * H <= 2^24, B * H * d <= 2^31, d <= 2^20,
- *    T < 2^30. TM_ERR_INVALID_ARG for bad arguments, TM_ERR_OOM for a
+ *    T <= 2^30 - 64, B * H * T * d <= 2^46; a stride <= 2^42, and <= 2^46 over its
+ *    whole dimension. TM_ERR_INVALID_ARG for bad arguments, TM_ERR_OOM for a
  *    workspace that is too small, TM_ERR_UNSUPPORTED for a problem that needs
  *    more than 2^31 - 1 thread blocks; none of these launches anything.
  */

@@ -36,7 +36,13 @@ bool separate(std::initializer_list<Buf> outs, std::initializer_list<Buf> ins) {
 
 bool aligned(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
-constexpr long long kMaxStride = 1LL << 42;
+// Elements from a tensor's first to its last along one dimension, and elements
+// of a call: far above any memory, and low enough that no sum or product of
+// them passes 64 bits (a scan's workspace holds up to 128 floats for each).
+constexpr long long kMaxExtent = 1LL << 46;
+constexpr long long kMaxStride = 1LL << 42;     // the kernels step some rows past the end in their addresses
+
+bool stride_ok(long long s, int n) { return s >= 0 && s <= kMaxStride && (n == 1 || s <= kMaxExtent / (n - 1)); }
 
 // Strides of tensor `i` of the caller's table, or contiguous [B, H, T, d].
 // A stride that moves over one element only is set to 0.
@@ -53,7 +59,7 @@ bool strides_of(const long long *table, int i, int B, int H, int T, long long d,
   if (B == 1) s->b = 0;
   if (H == 1) s->h = 0;
   if (T == 1) s->t = 0;
-  return s->b >= 0 && s->h >= 0 && s->t >= 0 && s->b <= kMaxStride && s->h <= kMaxStride && s->t <= kMaxStride;
+  return stride_ok(s->b, B) && stride_ok(s->h, H) && stride_ok(s->t, T);
 }
 
 size_t span(const Str &s, int B, int H, int T, long long d, int el) {
@@ -80,7 +86,7 @@ bool sizes_ok(int B, int H, int T, long long d, tm_dtype dt) {
   if (B < 1 || H < 1 || T < 1 || d < 1 || d > (1 << 20) || T > (1 << 30) - 64) return false;
   if (dt != TM_F32 && dt != TM_BF16) return false;
   if ((long long)B * H > (1LL << 24) || (long long)H * d > (1LL << 24)) return false;
-  return (long long)B * H * d <= (1LL << 33) / 4;
+  return (long long)B * H * d <= (1LL << 31) && (long long)B * H * d * T <= kMaxExtent;
 }
 bool act_ok(tm_act a) { return a == TM_ACT_SILU || a == TM_ACT_NONE; }
 int size_of(tm_dtype dt) { return dt == TM_BF16 ? 2 : 4; }
