@@ -47,6 +47,13 @@ def _named(table, name, value):
     return table[value]
 
 
+def _need(**tensors):
+    """Raises for the first that is not a tensor."""
+    for name, t in tensors.items():
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a tensor, got {type(t).__name__}")
+
+
 def _check(device, **tensors):
     """name=(tensor or None, shape, dtype, strided): raises for the first that has
     another shape, type or device, or that is not contiguous (its channels, if
@@ -117,6 +124,7 @@ def _elsewhere(fn, stream, x, args, kwargs):
     """fn on another device than the current one, or on a given stream: with both
     made current, so that what fn allocates belongs to them, and the allocator
     told that the stream uses the caller's tensors."""
+    _need(x=x)
     if not x.is_cuda:
         raise ValueError("x must be a CUDA tensor")
     with torch.cuda.device(x.device):
@@ -133,7 +141,7 @@ def _elsewhere(fn, stream, x, args, kwargs):
 
 def _here(x, stream):
     """Whether x's device is the current one and the call goes to its current stream."""
-    return stream is None and x.is_cuda and x.get_device() == torch.cuda.current_device()
+    return stream is None and isinstance(x, torch.Tensor) and x.is_cuda and x.get_device() == torch.cuda.current_device()
 
 
 # the current stream's handle, without a Stream object around it where torch offers that
@@ -160,6 +168,8 @@ def _workspace(given, x, fn, *sizes):
 
 def _conv_check(x, shape, filt, bias, hist, lengths, token2, tail):
     """Checks what the three convolution calls share; the width."""
+    if filt is None:
+        _need(filt=filt)
     w, dev, kind = filt.shape[-1], x.get_device(), x.dtype
     B, H, d = shape[0], shape[1], shape[-1]
     past = (B, H, w - 1, d)
@@ -204,6 +214,7 @@ def short_conv_backward(x, filt, dy, bias=None, *, hist=None, lengths=None, act=
                           dict(hist=hist, lengths=lengths, act=act, dtail=dtail, workspace=workspace))
     shape = B, H, T, d = _shape("x", x, 4)
     code = _dtype_code("x", x)
+    _need(dy=dy)
     w = _conv_check(x, shape, filt, bias, hist, lengths, dy, dtail)
     ws, n = _workspace(workspace, x, "tm_conv_backward_workspace_size", B, H, T, d, w, code)
     out = {"dx": torch.empty_like(x), "dfilt": torch.empty_like(filt)}
@@ -225,6 +236,8 @@ def short_conv_step(x, hist, filt, bias=None, *, act="silu", out=None, stream=No
         return _elsewhere(short_conv_step, stream, x, (hist, filt, bias), dict(act=act, out=out))
     shape = B, H, d = _shape("x", x, 3)
     code = _dtype_code("x", x)
+    if hist is None:
+        _need(hist=hist)
     w = _conv_check(x, shape, filt, bias, hist, None, out, None)
     if out is None:
         out = x.new_empty(shape)
@@ -236,6 +249,8 @@ def short_conv_step(x, hist, filt, bias=None, *, act="silu", out=None, stream=No
 
 def _scan_sizes(x, shape, dt, A, Bm, Cm, D, z, dt_bias, state, state2, token2, lengths):
     """Checks what the three scan calls share; (G, N)."""
+    if dt is None or A is None or Bm is None or Cm is None:
+        _need(dt=dt, A=A, Bm=Bm, Cm=Cm)
     kind, dev = x.dtype, x.get_device()
     B, H, d = shape[0], shape[1], shape[-1]
     if Bm.dim() != len(shape) or A.dim() != 3:
@@ -298,6 +313,7 @@ def selective_scan_backward(x, dt, A, Bm, Cm, dy, *, D=None, z=None, dt_bias=Non
                                softplus=softplus, workspace=workspace))
     shape = B, H, T, d = _shape("x", x, 4)
     code = _dtype_code("x", x)
+    _need(dy=dy)
     G, n = _scan_sizes(x, shape, dt, A, Bm, Cm, D, z, dt_bias, state, dstate_end, dy, lengths)
     ws, nb = _workspace(workspace, x, "tm_scan_backward_workspace_size", B, H, G, T, d, n, code)
     out = {"dx": torch.empty_like(x), "ddt": torch.empty_like(dt), "dA": torch.empty_like(A),
@@ -323,6 +339,8 @@ def selective_scan_step(x, dt, A, Bm, Cm, state, *, D=None, z=None, dt_bias=None
                           dict(D=D, z=z, dt_bias=dt_bias, softplus=softplus, out=out))
     shape = B, H, d = _shape("x", x, 3)
     code = _dtype_code("x", x)
+    if state is None:
+        _need(state=state)
     G, n = _scan_sizes(x, shape, dt, A, Bm, Cm, D, z, dt_bias, state, None, out, None)
     if out is None:
         out = x.new_empty(shape)
@@ -387,6 +405,7 @@ def group_norm_backward(x, dy, stats, weight=None, bias=None, *, over="token", a
         return _elsewhere(group_norm_backward, stream, x, (dy, stats, weight, bias),
                           dict(over=over, act=act, lengths=lengths, workspace=workspace))
     shape = B, H, T, d = _shape("x", x, 4)
+    _need(dy=dy, stats=stats)
     code, where, out_code = _dtype_code("x", x), _named(_OVER, "over", over), _dtype_code("dy", dy)
     _norm_check(x, shape, weight, bias, lengths, stats, over, dy, dy.dtype)
     ws, n = _workspace(workspace, x, "tm_group_norm_workspace_size", B, H, T, d, where, 1)
