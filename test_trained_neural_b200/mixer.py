@@ -156,6 +156,15 @@ def _workspace_size(fn, *sizes):
     return n.value
 
 
+def _like(x, dtype=None):
+    """An output for x: in x's layout where that is dense, with contiguous channels
+    always (x may repeat rows, or be overlapping windows of one signal)."""
+    out = torch.empty_like(x, dtype=dtype)
+    if out.stride(-1) != 1 and x.shape[-1] > 1:
+        out = torch.empty_like(x, dtype=dtype, memory_format=torch.contiguous_format)
+    return out
+
+
 def _workspace(given, x, fn, *sizes):
     """(tensor or None, bytes)"""
     if given is None:
@@ -196,7 +205,7 @@ def short_conv(x, filt, bias=None, *, hist=None, lengths=None, act="silu", out=N
     w = _conv_check(x, shape, filt, bias, hist, lengths, out, tail)
     fresh = out is None                                  # then rows behind the ends are written as zeros
     if fresh:
-        out = torch.empty_like(x)
+        out = _like(x)
     if tail is None:
         tail = x.new_empty((B, H, w - 1, d))
     N.check(N.load().tm_conv(B, H, T, d, w, code, _named(_ACTS, "act", act), fresh, x.data_ptr(), filt.data_ptr(), _p(bias),
@@ -217,7 +226,7 @@ def short_conv_backward(x, filt, dy, bias=None, *, hist=None, lengths=None, act=
     _need(dy=dy)
     w = _conv_check(x, shape, filt, bias, hist, lengths, dy, dtail)
     ws, n = _workspace(workspace, x, "tm_conv_backward_workspace_size", B, H, T, d, w, code)
-    out = {"dx": torch.empty_like(x), "dfilt": torch.empty_like(filt)}
+    out = {"dx": _like(x), "dfilt": torch.empty_like(filt)}
     if bias is not None:
         out["dbias"] = torch.empty_like(bias)
     if hist is not None:
@@ -290,7 +299,7 @@ def selective_scan(x, dt, A, Bm, Cm, *, D=None, z=None, dt_bias=None, state=None
     G, n = _scan_sizes(x, shape, dt, A, Bm, Cm, D, z, dt_bias, state, state_end, out, lengths)
     fresh = out is None
     if fresh:
-        out = torch.empty_like(x)
+        out = _like(x)
     if state_end is None:
         state_end = A.new_empty((B, H, d, n))
     ws, nb = _workspace(workspace, x, "tm_scan_workspace_size", B, H, G, T, d, n, code)
@@ -316,11 +325,11 @@ def selective_scan_backward(x, dt, A, Bm, Cm, dy, *, D=None, z=None, dt_bias=Non
     _need(dy=dy)
     G, n = _scan_sizes(x, shape, dt, A, Bm, Cm, D, z, dt_bias, state, dstate_end, dy, lengths)
     ws, nb = _workspace(workspace, x, "tm_scan_backward_workspace_size", B, H, G, T, d, n, code)
-    out = {"dx": torch.empty_like(x), "ddt": torch.empty_like(dt), "dA": torch.empty_like(A),
+    out = {"dx": _like(x), "ddt": _like(dt), "dA": torch.empty_like(A),
            "dB": x.new_empty((B, G, T, n)), "dC": x.new_empty((B, G, T, n))}
     for name, t in (("dD", D), ("dz", z), ("ddt_bias", dt_bias), ("dstate", state)):
         if t is not None:
-            out[name] = torch.empty_like(t)
+            out[name] = _like(t)
     N.check(N.load().tm_scan_backward(
         B, H, G, T, d, n, code, bool(softplus), _p(x), _p(dt), _p(A), _p(Bm), _p(Cm), _p(D), _p(z), _p(dt_bias),
         _p(state), _p(lengths), _p(dy), _p(dstate_end), _p(out["dx"]), _p(out["ddt"]), _p(out["dA"]), _p(out["dB"]),
@@ -386,7 +395,7 @@ def group_norm(x, weight=None, bias=None, *, over="token", act=None, eps=1e-5, l
     kept = _norm_check(x, shape, weight, bias, lengths, stats, over, out, kind)
     fresh = out is None
     if fresh:
-        out = torch.empty_like(x, dtype=kind)
+        out = _like(x, kind)
     if stats is None:
         # rows behind the ends: written with those of y, so zeroed here when those of a given y are left alone
         stats = (x.new_empty if lengths is None or fresh else x.new_zeros)(kept, dtype=_F32)
@@ -409,7 +418,7 @@ def group_norm_backward(x, dy, stats, weight=None, bias=None, *, over="token", a
     code, where, out_code = _dtype_code("x", x), _named(_OVER, "over", over), _dtype_code("dy", dy)
     _norm_check(x, shape, weight, bias, lengths, stats, over, dy, dy.dtype)
     ws, n = _workspace(workspace, x, "tm_group_norm_workspace_size", B, H, T, d, where, 1)
-    out = {"dx": torch.empty_like(x)}
+    out = {"dx": _like(x)}
     if weight is not None:
         out["dweight"] = torch.empty_like(weight)
     if bias is not None:
