@@ -6,17 +6,16 @@
 //   dx = r (k - mean(k) - xh mean(k xh)),  dweight = sum dy act'(p) xh,  dbias = sum dy act'(p)
 // One token: a row's channels sit in the registers of LPR lanes, so x is read
 // once, and mean and variance are two passes over registers. A sequence: one
-// pass for the statistics (per-thread sums about the thread's first value,
-// joined as (count, mean, sum of squared differences)), one for the output,
-// which finds most of x in L2. HBM bounds it, and close behind it the issue
-// slots: two channels per instruction. The parameters' gradients leave each CTA
+// pass for the statistics (joined as (count, mean, sum of squared differences)),
+// one for the output, which finds most of x in L2. HBM bounds it, and close behind
+// it the issue slots: two channels per instruction. The parameters' gradients leave each CTA
 // as one partial and are summed in a fixed order. Grids are one wave of CTAs
 // that walk their rows with the next ones in flight. Measured on B200:
 //   token by token, 4 x 8 x 8192 x 64 bf16, SiLU: 15.6 us, 4.4 TB/s (a CTA per
 //     128 rows: 18.2 us);
 //   its gradient, 8 x 8 x 8192 x 128 bf16: 84 us + 2.5 us for the sums, 4.8 TB/s
 //     (256-thread CTAs in 4.1 waves: 96 us; one channel per instruction: 109 us);
-//   a sequence, 2 x 4001 x 1536 fp32, 32 groups: 10.8 + 4.8 + 13.7 us.
+//   a sequence, 2 x 4001 x 1536 fp32, 32 groups: 28.7 us, three launches.
 #include "tm_mixer.cuh"
 
 namespace tmem {
@@ -405,10 +404,25 @@ __device__ __forceinline__ At at_of(const Norm &a, const Cols &s, int V) {
   return q;
 }
 
+// (count, mean, sum of squares about the mean) of two sets of values together.
+__device__ __forceinline__ void join(float3 &t, const float3 &o) {
+  const float nn = t.x + o.x, dm = o.y - t.y, f = __fdividef(o.x, nn);
+  t.z += o.z + dm * (t.x * f) * dm;                      // 0 for t empty, however large the means
+  t.y += dm * f;
+  t.x = nn;
+}
+
 // Statistics: (count, mean, sum of squares about the mean) of each vector
-// column and row tile, [b][tile][H d / V].
+// column and row tile, [b][tile][H d / V]. A thread joins its rows 8 at a time;
+// each batch is summed about the mean of two of its channels. So a sum is short,
+// and its squares come to at most 64 / 16 times what they are about the batch's
+// mean (those 16 values far from the rest). One sum of up to 512 values about the
+// first of them lost 9 bits when that one was far from the rest, as a first token
+// may be: 571 u off in 1 / sqrt(variance) where this is within 64 u. The three
+// launches so, and about one value: 4 x 8 x 8192 x 64 bf16 26.7 and 24.7 us, fp32
+// 43.6 and 47.7 us (a batch is loaded whole before its first use).
 template <typename TI, int V>
-__global__ void __launch_bounds__(NT) seq_stats_kernel(const Norm a, const Cols s, float2 *part) {
+__global__ void __launch_bounds__(NT, 2) seq_stats_kernel(const Norm a, const Cols s, float2 *part) {
   __shared__ float3 red[NT];
   let_next_start();
   const At q = at_of(a, s, V);
@@ -418,30 +432,32 @@ __global__ void __launch_bounds__(NT) seq_stats_kernel(const Norm a, const Cols 
     const TI *x = static_cast<const TI *>(a.x) + q.b * a.sx.b + q.h0 * a.sx.h + q.c;
     const long long t0 = ((long long)q.tile * s.RL + q.rl) * s.run;
     const long long t1 = t0 + s.run < n ? t0 + s.run : n;
-    if (t0 < t1) {
-      float k = 0.f;
-      F2 p1 = both(0.f), p2 = both(0.f);
-      for (long long t = t0; t < t1; t += 8) {
-        Vec<TI, V> raw[8];
+    for (long long t = t0; t < t1; t += 8) {
+      Vec<TI, V> raw[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) raw[i] = load_if<TI, V>(x + (t + i) * a.sx.t, t + i < t1);
-        if (t == t0) k = get(raw[0], 0);
+      for (int i = 0; i < 8; ++i) raw[i] = load_if<TI, V>(x + (t + i) * a.sx.t, t + i < t1);
+      Pairs<V> u;
+      F2 f = both(0.f), p1 = both(0.f), p2 = both(0.f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (t + i < t1) {
-            Pairs<V> u;
-            to_pairs<V>(u, raw[i]);
-#pragma unroll
-            for (int e = 0; e < (V + 1) / 2; ++e) {
-              const F2 q = add(u[e], both(-k));
-              p1 = add(p1, q);
-              p2 = fma(q, q, p2);
-            }
-          }
+      for (int i = 0; i < 8; ++i) {
+        to_pairs<V>(u, raw[i]);                          // rows past the run are zeros
+        f = add(f, u[0]);
       }
-      const float s1 = total<V>(p1), s2 = total<V>(p2);
-      const float cnt = (float)((t1 - t0) * V), mean = s1 / cnt;
-      mine = make_float3(cnt, k + mean, fmaxf(s2 - s1 * mean, 0.f));
+      const int rows = t1 - t < 8 ? (int)(t1 - t) : 8;
+      const float about = __fdividef(total<V>(f), (float)(rows * (V < 2 ? V : 2)));
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (t + i < t1) {
+          to_pairs<V>(u, raw[i]);
+#pragma unroll
+          for (int e = 0; e < (V + 1) / 2; ++e) {
+            u[e] = add(u[e], both(-about));
+            p1 = add(p1, u[e]);
+            p2 = fma(u[e], u[e], p2);
+          }
+        }
+      const float cnt = (float)(rows * V), s1 = total<V>(p1), left = __fdividef(s1, cnt);
+      join(mine, make_float3(cnt, about + left, fmaxf(fmaf(-s1, left, total<V>(p2)), 0.f)));
     }
   }
   red[threadIdx.x] = mine;
@@ -450,11 +466,7 @@ __global__ void __launch_bounds__(NT) seq_stats_kernel(const Norm a, const Cols 
   float3 t = red[threadIdx.x];
   for (int r = 1; r < s.RL; ++r) {
     const float3 o = red[r * s.nvb + q.vi];
-    if (o.x == 0.f) continue;
-    const float nn = t.x + o.x, dm = o.y - t.y, f = o.x / nn;
-    t.z += o.z + dm * dm * t.x * f;
-    t.y += dm * f;
-    t.x = nn;
+    if (o.x != 0.f) join(t, o);
   }
   const long long vecs = (long long)a.H * a.d / V;
   part[((long long)q.b * s.tiles + q.tile) * vecs + q.h0 * (a.d / V) + q.v] = make_float2(t.y, t.z);
