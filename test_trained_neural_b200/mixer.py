@@ -141,10 +141,13 @@ def _elsewhere(fn, stream, x, args, kwargs):
 
 def _here(x, stream):
     """Whether x's device is the current one and the call goes to its current stream."""
-    return stream is None and isinstance(x, torch.Tensor) and x.is_cuda and x.get_device() == torch.cuda.current_device()
+    return stream is None and isinstance(x, _Tensor) and x.is_cuda and x.get_device() == _current_device()
 
 
-# the current stream's handle, without a Stream object around it where torch offers that
+_Tensor = torch.Tensor
+# the current device and stream without the checks and the Stream object around them, where torch offers that
+# (a CUDA tensor is there: CUDA is initialised)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
@@ -159,9 +162,9 @@ def _workspace_size(fn, *sizes):
 def _like(x, dtype=None):
     """An output for x: in x's layout where that is dense, with contiguous channels
     always (x may repeat rows, or be overlapping windows of one signal)."""
-    out = torch.empty_like(x, dtype=dtype)
-    if out.stride(-1) != 1 and x.shape[-1] > 1:
-        out = torch.empty_like(x, dtype=dtype, memory_format=torch.contiguous_format)
+    out = torch.empty_like(x) if dtype is None else torch.empty_like(x, dtype=dtype)
+    if not x.is_contiguous() and out.stride(-1) != 1 and x.shape[-1] > 1:
+        out = torch.empty_like(out, memory_format=torch.contiguous_format)
     return out
 
 
@@ -223,7 +226,8 @@ def short_conv_backward(x, filt, dy, bias=None, *, hist=None, lengths=None, act=
                           dict(hist=hist, lengths=lengths, act=act, dtail=dtail, workspace=workspace))
     shape = B, H, T, d = _shape("x", x, 4)
     code = _dtype_code("x", x)
-    _need(dy=dy)
+    if dy is None:
+        _need(dy=dy)
     w = _conv_check(x, shape, filt, bias, hist, lengths, dy, dtail)
     ws, n = _workspace(workspace, x, "tm_conv_backward_workspace_size", B, H, T, d, w, code)
     out = {"dx": _like(x), "dfilt": torch.empty_like(filt)}
@@ -322,14 +326,17 @@ def selective_scan_backward(x, dt, A, Bm, Cm, dy, *, D=None, z=None, dt_bias=Non
                                softplus=softplus, workspace=workspace))
     shape = B, H, T, d = _shape("x", x, 4)
     code = _dtype_code("x", x)
-    _need(dy=dy)
+    if dy is None:
+        _need(dy=dy)
     G, n = _scan_sizes(x, shape, dt, A, Bm, Cm, D, z, dt_bias, state, dstate_end, dy, lengths)
     ws, nb = _workspace(workspace, x, "tm_scan_backward_workspace_size", B, H, G, T, d, n, code)
     out = {"dx": _like(x), "ddt": _like(dt), "dA": torch.empty_like(A),
            "dB": x.new_empty((B, G, T, n)), "dC": x.new_empty((B, G, T, n))}
-    for name, t in (("dD", D), ("dz", z), ("ddt_bias", dt_bias), ("dstate", state)):
+    if z is not None:
+        out["dz"] = _like(z)
+    for name, t in (("dD", D), ("ddt_bias", dt_bias), ("dstate", state)):
         if t is not None:
-            out[name] = _like(t)
+            out[name] = torch.empty_like(t)
     N.check(N.load().tm_scan_backward(
         B, H, G, T, d, n, code, bool(softplus), _p(x), _p(dt), _p(A), _p(Bm), _p(Cm), _p(D), _p(z), _p(dt_bias),
         _p(state), _p(lengths), _p(dy), _p(dstate_end), _p(out["dx"]), _p(out["ddt"]), _p(out["dA"]), _p(out["dB"]),
@@ -414,7 +421,8 @@ def group_norm_backward(x, dy, stats, weight=None, bias=None, *, over="token", a
         return _elsewhere(group_norm_backward, stream, x, (dy, stats, weight, bias),
                           dict(over=over, act=act, lengths=lengths, workspace=workspace))
     shape = B, H, T, d = _shape("x", x, 4)
-    _need(dy=dy, stats=stats)
+    if dy is None or stats is None:
+        _need(dy=dy, stats=stats)
     code, where, out_code = _dtype_code("x", x), _named(_OVER, "over", over), _dtype_code("dy", dy)
     _norm_check(x, shape, weight, bias, lengths, stats, over, dy, dy.dtype)
     ws, n = _workspace(workspace, x, "tm_group_norm_workspace_size", B, H, T, d, where, 1)
