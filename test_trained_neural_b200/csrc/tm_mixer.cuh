@@ -205,11 +205,6 @@ __device__ __forceinline__ F2 softplus(F2 v) {
   p = fma(p, u, both(9.999999659e-01f));
   return fma(u, p, pair(fmaxf(a, 0.f), fmaxf(b, 0.f)));
 }
-__device__ __forceinline__ float softplus(float v) {
-  float a, b;
-  unpair(a, b, softplus(both(v)));
-  return a;
-}
 
 // f of every value, two at a time
 template <int V, typename F>

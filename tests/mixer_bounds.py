@@ -10,6 +10,7 @@ and with its argument's rounding |p| U more; silu'(p) is within 1.2, silu''(p) w
 import torch
 
 U = 2.0 ** -24
+TINY = 2.0 ** -126       # results of the special-function unit below this are flushed to 0
 
 
 def half(kind):
@@ -26,7 +27,7 @@ class rounded:
         assert got.shape == self.ref.shape, (what, got.shape, self.ref.shape)
         assert torch.isfinite(got).all(), what
         # half a step of what is rounded, which is itself off by the bound; denormal results may be flushed
-        allowed = self.bound + half(got.dtype) * (self.ref.abs() + self.bound) + 2.0 ** -126
+        allowed = self.bound + half(got.dtype) * (self.ref.abs() + self.bound) + TINY
         d = (got.double() - self.ref).abs()
         assert (d <= allowed).all(), (what, (d / allowed).max().item())
 
@@ -186,7 +187,7 @@ def scan(x, dt, A, Bm, Cm, D, z, dt_bias, state, dy, dstate_end, lengths, segmen
         a, rd = decay(t)
         ub = (e[:, :, t] * X[:, :, t])[..., None] * Bs[:, :, t, None]
         m = a * hmax[-1] + ub.abs()
-        err = a * es[-1] + rd * a * hmax[-1] + (re[:, :, t, :, None] + 3 * U) * ub.abs() + 2 * U * m * on[:, :, t, :, None]
+        err = a * es[-1] + (rd * a + TINY) * hmax[-1] + (re[:, :, t, :, None] + 3 * U) * ub.abs() + 2 * U * m * on[:, :, t, :, None]
         hs.append(a * hs[-1] + ub)
         es.append(err)
         hmax.append(m)
@@ -223,7 +224,7 @@ def scan(x, dt, A, Bm, Cm, D, z, dt_bias, state, dy, dstate_end, lengths, segmen
         du[:, :, t] = (g * B_).sum(-1)
         duerr[:, :, t] = (gerr * B_.abs() + (N + 2) * U * gmax * B_.abs()).sum(-1)
         R, Rmax = g * a, gmax * a
-        Rerr = a * gerr + rd * Rmax + U * Rmax * on[:, :, t, :, None]
+        Rerr = a * gerr + rd * Rmax + TINY * gmax + U * Rmax * on[:, :, t, :, None]
         q, qmax = R * hs[t], Rmax * hmax[t]
         qerr = Rerr * hmax[t] + Rmax * es[t] + 2 * U * qmax
         de[:, :, t] = X[:, :, t] * du[:, :, t] + (Ad * q).sum(-1)

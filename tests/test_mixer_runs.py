@@ -258,3 +258,29 @@ def test_replayed_on_other_inputs(kind):
         torch.cuda.synchronize()
         for i, (p, q) in enumerate(zip(got, want)):
             assert torch.equal(p, q), i
+
+
+@gpu
+def test_steps_on_a_given_stream():
+    """`stream=`: the step waits for nothing but its stream, updates hist and state there, and its output belongs to it."""
+    B, H, d, N = 64, 4, 96, 16
+    r = Draw("step stream")
+    x, dt, z = (r.normal(B, H, d, kind=BF) for _ in range(3))
+    f, A = r.normal(H, d, 4), -r.uniform(0.5, 4, H, d, N)
+    Bm, Cm = r.normal(B, 2, N, kind=BF), r.normal(B, 2, N, kind=BF)
+    hist, state = r.normal(B, H, 3, d, kind=BF), r.normal(B, H, d, N)
+    h, s = [[t.clone() for _ in range(2)] for t in (hist, state)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(20):
+        q = tm.short_conv_step(x, h[0], f, stream=side)
+        got += [q, tm.selective_scan_step(q, dt, A, Bm, Cm, s[0], z=z, stream=side)]
+        junk = torch.full((B, H, d), float("nan"), device="cuda", dtype=BF)   # the current stream's memory, not the side's
+        del junk
+    side.synchronize()
+    for i in range(20):
+        q = tm.short_conv_step(x, h[1], f)
+        y = tm.selective_scan_step(q, dt, A, Bm, Cm, s[1], z=z)
+        assert torch.equal(q, got[2 * i]) and torch.equal(y, got[2 * i + 1])
+    assert torch.equal(h[0], h[1]) and torch.equal(s[0], s[1])
