@@ -11,10 +11,11 @@
 // the w - 1 rows before a run come from L2. Measured on B200, bf16, w = 4:
 //   forward, 65536 x 2048 (16 heads of 128 in [T, H, d] rows): 93 us, 5.8 TB/s
 //     (with rows by plain loads one batch ahead: 109 us; short runs: 111 us);
-//   gradient, 4 x 8 x 8192 x 64: 29 us + 3 us for the sums, 3.1 TB/s, bound by
-//     latency at 12 warps an SM (a run is 76 rows at this size; slots in shared
-//     memory as in the forward measured 34 us);
-//   one token, 64 x 1536: 2.3 us, a launch.
+//   gradient, 4 x 8 x 8192 x 64: 33 us, of which 3 us are the sums, 3.1 TB/s, bound
+//     by latency at 10.6 warps an SM: 168 registers, 56 bytes of a thread spilled
+//     (a run is 76 rows at this size; slots in shared memory as in the forward
+//     measured 34 us for the first kernel's 29);
+//   one token, 64 x 1536: a kernel of 2.2 us, 4.1 us a call replayed from a graph.
 #include <type_traits>
 
 #include "tm_mixer.cuh"

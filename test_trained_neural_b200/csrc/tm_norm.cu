@@ -11,9 +11,9 @@
 // it the issue slots: two channels per instruction. The parameters' gradients leave each CTA
 // as one partial and are summed in a fixed order. Grids are one wave of CTAs
 // that walk their rows with the next ones in flight. Measured on B200:
-//   token by token, 4 x 8 x 8192 x 64 bf16, SiLU: 15.6 us, 4.4 TB/s (a CTA per
-//     128 rows: 18.2 us);
-//   its gradient, 8 x 8 x 8192 x 128 bf16: 84 us + 2.5 us for the sums, 4.8 TB/s
+//   token by token, 4 x 8 x 8192 x 64 bf16, SiLU: 16.5 us, 4.1 TB/s, the issue
+//     slots at 0.64, the special-function unit at 0.60 (a CTA per 128 rows 18.2 us);
+//   its gradient, 8 x 8 x 8192 x 128 bf16: 84 us + 2.5 us for the sums, 4.7 TB/s
 //     (256-thread CTAs in 4.1 waves: 96 us; one channel per instruction: 109 us);
 //   a sequence, 2 x 4001 x 1536 fp32, 32 groups: 28.7 us, three launches.
 #include "tm_mixer.cuh"

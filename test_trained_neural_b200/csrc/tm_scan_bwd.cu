@@ -24,6 +24,9 @@
 // special-function unit 0.38: the dependent chains of a chunk bound it. Holding
 // the decays of a chunk instead of evaluating them again spills (513 us); chunks
 // of 8 at 8 warps an SM took 609 us; the states in shared memory at 16 warps 407.
+// With more than 64 states the registers do not hold a lane's share: up to 348
+// (first pass) and 272 bytes (second) of a thread are spilled. 4 x 8 x 1024 x 64
+// fp32 with 128 states takes 1280 us, 4 x 8 x 2048 x 64 bf16 with 64 840 us.
 #include "tm_scan.cuh"
 
 namespace tmem {
@@ -52,8 +55,10 @@ Plan plan_of(int B, int H, int G, int T, int d, int N) {
   p.NP = NL * SPL;
   p.warps = d <= 2 * CW ? 2 : MAXW;
   p.blocks = (d + CW * p.warps - 1) / (CW * p.warps);
-  // three CTAs of 4 warps fit on an SM; a split costs the first pass the
-  // gradient sums and the joins, so it has to at least double the CTAs
+  // Three CTAs of 4 warps fit on an SM (two of the second pass in fp32 with up to 8
+  // states, whose shared memory is 93 KB: large problems of that kind then run
+  // in one and a half waves); a split costs the first pass the gradient sums and
+  // the joins, so it has to at least double the CTAs
   const long long ctas = (long long)B * H * p.blocks * p.warps / MAXW + 1;
   long long S = 3LL * kSMs / ctas;
   const long long most = T / TF;

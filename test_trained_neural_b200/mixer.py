@@ -7,7 +7,8 @@ float32 or bfloat16, with contiguous channels and any other strides: a
 [B, T, H, d] tensor is passed as x.transpose(1, 2), a slice of a projection as
 it is. Parameters, states and statistics are contiguous float32. Every function
 runs on `stream` (default: the current stream of the tensors' device) and takes
-its outputs and workspace from torch unless they are given.
+its outputs and workspace from torch unless they are given. Gradients are calls
+of their own (`*_backward`): outputs never require gradients, whatever the inputs do.
 
 `lengths` ([B] int32 on the device) gives the tokens of each sequence of a
 padded batch: rows behind them are not read, and are zero in outputs that are
