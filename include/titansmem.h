@@ -363,8 +363,8 @@ TM_API tm_status tm_prologue(int B, int H, int T, int d, int width, tm_dtype in_
  *  - Pointers are aligned to their elements (workspaces to 256 bytes); wide
  *    loads are used where bases, strides and sizes allow. d need not be a
  *    multiple of anything.
- *  - A value that is not finite, or a step that is not, leaves what depends on it
- *    not finite; which of infinity and NaN it becomes is not specified.
+ *  - NaN spreads to what depends on it; an infinity, or a square or product past
+ *    fp32's range, may come out as NaN.
  *  - Outputs must not overlap inputs or one another (judged by the range from
  *    first to last element), except state_end == state0 exactly in tm_scan.
  *  - The calls are asynchronous on `stream` of the current device, allocate

@@ -457,7 +457,8 @@ __global__ void __launch_bounds__(NT, 2) seq_stats_kernel(const Norm a, const Co
           }
         }
       const float cnt = (float)(rows * V), s1 = total<V>(p1), left = __fdividef(s1, cnt);
-      join(mine, make_float3(cnt, about + left, fmaxf(fmaf(-s1, left, total<V>(p2)), 0.f)));
+      const float m2 = fmaf(-s1, left, total<V>(p2));
+      join(mine, make_float3(cnt, about + left, m2 < 0.f ? 0.f : m2));   // a NaN stays one
     }
   }
   red[threadIdx.x] = mine;
@@ -510,8 +511,9 @@ __global__ void __launch_bounds__(NT) seq_join_kernel(const Norm a, const Cols s
   s1 = all(s1, 0);
   s2 = all(s2, 1);
   if (threadIdx.x == 0) {
-    const double mean = n > 0 ? s1 / cnt : 0., var = n > 0 ? fmax(s2 / cnt - mean * mean, 0.) : 0.;
-    stats[bh] = n > 0 ? make_float2((float)mean, (float)(1. / sqrt(var + (double)a.eps))) : make_float2(0.f, 0.f);
+    const double mean = s1 / cnt, var = s2 / cnt - mean * mean;
+    stats[bh] = n > 0 ? make_float2((float)mean, (float)(1. / sqrt((var < 0. ? 0. : var) + (double)a.eps)))
+                      : make_float2(0.f, 0.f);
   }
 }
 

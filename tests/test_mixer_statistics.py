@@ -41,3 +41,19 @@ def test_statistics_beside_outliers(B, H, T, d, kind, where):
     # the mean's error is 64 u of the spread and its rounding, the factor's as above
     far = (m.abs() * rstd)[..., None, None]
     assert ((y - want).abs() <= 64 * U * (2 + want.abs()) + U * far * (2 + 1.1 * want.abs())).all()
+
+
+@pytest.mark.parametrize("B,H,T,d", [(2, 3, 900, 20), (1, 2, 40, 7)])
+def test_squares_past_fp32_do_not_become_a_variance_of_nothing(B, H, T, d):
+    """Values of 1e25, whose squares overflow: not a factor of 1 / sqrt(eps) and finite outputs made with it. A NaN
+    reaches the statistics and outputs of its own group, and no other."""
+    x = Draw("overflow", B, H, T, d).normal(B, H, T, d)
+    y, stats = tm.group_norm(x * 1e25, over="sequence")
+    assert not (stats[..., 1] > 1e-18).any() and not (y.abs() > 1e6).any()
+    want = tm.group_norm(x, over="sequence")
+    x[0, 1, T // 2, 3] = float("nan")
+    got = tm.group_norm(x, over="sequence")
+    for p, q in zip(got, want):
+        assert torch.isnan(p[0, 1]).all()
+        p[0, 1] = q[0, 1]
+        assert torch.equal(p, q)
